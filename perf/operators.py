@@ -106,6 +106,7 @@ def _quantise(x, kind):
     amax = x.abs().amax(-1)
     fine = torch.isfinite(amax)
     held = torch.where(fine, amax, 1.0).clamp(min=_TINY)
+    top = torch.full_like(held, top)  # a quotient of tensors is rounded once, one with a number is not
     y = torch.where(fine.unsqueeze(-1), x * (top / held).unsqueeze(-1), 0.0)
     code = y.to(E4M3) if kind == "e4m3" else y.round().to(I8)
     return code, torch.where(fine, held / top, math.nan)
