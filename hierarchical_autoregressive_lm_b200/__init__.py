@@ -18,7 +18,8 @@ from typing import Optional
 __all__ = ["PhotonError", "Model", "Cache", "load_library", "LIB_PATH", "MODE_HIER",
            "MODE_REC", "STATE", "launch_count", "gemm", "gemm_rmsnorm", "attn_decode", "attn_decode_noalloc", "attn_prefill", "attn_decode_scratch_bytes", "debug_fail_alloc",
            "selftest_wait_timeout", "config_struct", "EXPORTED",
-           "AGG_VOTE", "AGG_BEST", "aggregate", "ENC_RESTORE", "ENC_REGENERATE", "ENC_KEEP"]
+           "AGG_VOTE", "AGG_BEST", "aggregate", "ENC_RESTORE", "ENC_REGENERATE", "ENC_KEEP",
+           "Rope", "KVPages", "rope", "kv_write", "kv_read", "attn_decode_paged"]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libphoton.so")
 
@@ -43,7 +44,9 @@ EXPORTED = ("photon_init_weights", "photon_free_model", "photon_prefill",
             "photon_vanilla_free_cache", "photon_launch_count", "photon_last_error",
             "photon_debug_fail_alloc", "photon_selftest_wait_timeout", "photon_init_weights_levels",
             "photon_model_set_encoder_residency", "photon_prefill_shell", "photon_cache_state_buffer",
-            "photon_attn_prefill", "photon_model_set_kv_pages", "photon_prefill_paged")
+            "photon_attn_prefill", "photon_model_set_kv_pages", "photon_prefill_paged",
+            "photon_rope_frequencies", "photon_rope", "photon_kv_write", "photon_kv_read",
+            "photon_attn_decode_paged")
 
 
 class PhotonError(RuntimeError):
@@ -104,6 +107,23 @@ class photon_vanilla_stats(ctypes.Structure):
                [("kv_bytes", ctypes.c_uint64), ("workspace_bytes", ctypes.c_uint64)]
 
 
+class photon_rope_config(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("rot_dim", "scaling", "original_len")] + \
+               [(n, ctypes.c_double) for n in ("theta", "factor", "alpha", "beta", "attn_scale")]
+
+
+class photon_rope_table(ctypes.Structure):
+    _fields_ = [("d_freq", ctypes.c_void_p), ("rot_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                ("scale", ctypes.c_float)]
+
+
+class photon_kv_pages(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("k", "v", "k_scale", "v_scale")] + \
+               [(n, ctypes.c_int64) for n in ("page_stride", "head_stride", "row_stride", "scale_page",
+                                              "scale_head", "scale_row")] + \
+               [(n, ctypes.c_int32) for n in ("kind", "pages", "page_rows", "heads", "head_dim")]
+
+
 _lib: Optional[ctypes.CDLL] = None
 
 
@@ -156,6 +176,13 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         "photon_model_set_encoder_residency": [P, I32],
         "photon_init_weights_levels": [ctypes.POINTER(photon_level_config), U64, ctypes.POINTER(P)],
         "photon_selftest_wait_timeout": [I64, P, P],
+        "photon_rope_frequencies": [ctypes.POINTER(photon_rope_config), P, ctypes.POINTER(ctypes.c_float)],
+        "photon_rope": [I32, P, P, I32, I32, P, I64, I64, I32, P, I64, I64, P, I64, I64, I32, P, I64, I64, I32, P],
+        "photon_kv_write": [P, I32, P, I64, I32, I32, P, P, I32, P, I64, I64, P, I64, I64, P, P, I64, I64, I32, P,
+                            I64, I64, P, P],
+        "photon_kv_read": [P, I32, P, I64, I32, I32, P, P, I32, P, I64, I64, P, I64, I64, P, P],
+        "photon_attn_decode_paged": [P, I32, P, I64, I32, I32, P, P, I64, I64, I32, I32, ctypes.c_float, P, I64, I64,
+                                     P, P, P],
     }
     for name, args in sig.items():
         fn = getattr(L, name)
@@ -655,6 +682,256 @@ def attn_decode_scratch_bytes(dtype_code: int, G: int, H: int, head_dim: int, ca
     _check(load_library().photon_attn_decode_scratch_bytes(dtype_code, G, H, head_dim, cap, q_len, p0,
                                                            ctypes.byref(out)))
     return int(out.value)
+
+
+def _rows(t, dtype, shape: tuple, name: str, out: bool = False) -> tuple:
+    """Host-side check of a strided tensor of rows (last dimension contiguous); its strides."""
+    import torch
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch tensor, got {type(t).__name__}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name}: expected {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name}: expected shape {list(shape)}, got {list(t.shape)}")
+    st = t.stride()
+    if st[-1] != 1 and shape[-1] > 1:
+        raise ValueError(f"{name}: the last dimension must be contiguous")
+    if out and 0 in st and any(s == 0 and n > 1 for s, n in zip(st, shape)):
+        raise ValueError(f"{name}: an output cannot be an expanded tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name}: must be a CUDA tensor")
+    return st
+
+
+def _launch(fn, tensors, stream, args) -> None:
+    """fn(*args, stream) on the device of the tensors, which must be one."""
+    import torch
+    dev = tensors[0].device
+    for t in tensors:
+        if t is not None and t.device != dev:
+            raise ValueError(f"tensors on {dev} and {t.device}")
+    if stream is None:
+        stream = torch.cuda.current_stream(dev)
+    s = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    if dev.index == torch.cuda.current_device():
+        _check(fn(*args, s))
+    else:
+        with torch.cuda.device(dev):
+            _check(fn(*args, s))
+
+
+def _code(t, name: str) -> int:
+    import torch
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch tensor, got {type(t).__name__}")
+    if t.dtype == torch.bfloat16:
+        return 1
+    if t.dtype == torch.float32:
+        return 0
+    raise ValueError(f"{name}: expected torch.float32 or torch.bfloat16, got {t.dtype}")
+
+
+class Rope:
+    """Rotary positions (photon_rope_config): the first rot_dim elements of a head turn,
+    in pairs (i, i + rot_dim/2), or (2i, 2i + 1) when interleaved.  scaling: "none",
+    "linear", "ntk" or "yarn" with its factor (yarn: original_len, alpha, beta);
+    attn_scale 0 = the scaling's own."""
+
+    SCALING = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}
+
+    def __init__(self, rot_dim: int, theta: float = 10000.0, interleaved: bool = False, scaling: str = "none",
+                 factor: float = 1.0, original_len: int = 0, alpha: float = 1.0, beta: float = 32.0,
+                 attn_scale: float = 0.0, device="cuda"):
+        import torch
+        if scaling not in self.SCALING:
+            raise ValueError(f"scaling: expected one of {list(self.SCALING)}, got {scaling!r}")
+        self.rot_dim, self.interleaved = int(rot_dim), bool(interleaved)
+        cfg = photon_rope_config(self.rot_dim, self.SCALING[scaling], int(original_len), float(theta), float(factor),
+                                 float(alpha), float(beta), float(attn_scale))
+        host = (ctypes.c_uint64 * max(1, self.rot_dim // 2))()
+        scale = ctypes.c_float()
+        _check(load_library().photon_rope_frequencies(ctypes.byref(cfg), host, ctypes.byref(scale)))
+        self.turns, self.scale = list(host), float(scale.value)  # 2^64 * turns a position, on the host
+        self.freq = torch.tensor([x - (1 << 64) if x >> 63 else x for x in host], dtype=torch.int64).to(device)
+        if self.freq.is_cuda:
+            torch.cuda.current_stream(self.freq.device).synchronize()  # ready for every stream
+        self._t = photon_rope_table(self.freq.data_ptr(), self.rot_dim, int(self.interleaved), self.scale)
+        self._ref = ctypes.addressof(self._t)
+
+
+class KVPages:
+    """A pool of key and value pages of one layer in the caller's tensors (photon_kv_pages):
+    k, v [pages, heads, page_rows, head_dim] of any strides (the last dimension contiguous,
+    the others multiples of 16 bytes; both alike), float32, bfloat16, or narrow:
+    float8_e4m3fn or int8 with k_scale, v_scale float32 [pages, heads, page_rows]."""
+
+    def __init__(self, k, v, k_scale=None, v_scale=None):
+        import torch
+        kinds = {torch.float32: 0, torch.bfloat16: 1, torch.float8_e4m3fn: 2, torch.int8: 3}
+        for t, name in ((k, "k"), (v, "v")):
+            if not isinstance(t, torch.Tensor):
+                raise TypeError(f"{name}: expected a torch tensor, got {type(t).__name__}")
+            if t.dtype not in kinds or t.dim() != 4:
+                raise ValueError(f"{name}: expected [pages, heads, page_rows, head_dim] of {list(kinds)}")
+        kind = kinds[k.dtype]
+        if v.dtype != k.dtype or v.shape != k.shape:
+            raise ValueError(f"v: expected {k.dtype} of shape {list(k.shape)}, as k")
+        scales = (k_scale, v_scale)
+        if (kind >= 2) != all(s is not None for s in scales) or (kind < 2 and any(s is not None for s in scales)):
+            raise ValueError("k_scale and v_scale go with 8-bit pages, and only with them")
+        shape = tuple(k.shape)
+        st = _rows(k, k.dtype, shape, "k", out=True)
+        if _rows(v, k.dtype, shape, "v", out=True) != st:
+            raise ValueError("k and v must have the same strides")
+        ss = (0, 0, 0)
+        for s, name in zip(scales, ("k_scale", "v_scale")):
+            if s is not None:
+                if s.dtype != torch.float32 or tuple(s.shape) != shape[:3] or not s.is_cuda:
+                    raise ValueError(f"{name}: expected CUDA torch.float32 {list(shape[:3])}")
+                if any(a == 0 and n > 1 for a, n in zip(s.stride(), shape)):
+                    raise ValueError(f"{name}: an output cannot be an expanded tensor")
+        if kind >= 2:
+            ss = k_scale.stride()
+            if v_scale.stride() != ss:
+                raise ValueError("k_scale and v_scale must have the same strides")
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.pages, self.heads, self.page_rows, self.head_dim = shape
+        self.dtype, self.device = k.dtype, k.device
+        if any(t is not None and t.device != self.device for t in (v, *scales)):
+            raise ValueError("k, v and their scales must be on one device")
+        self._wide = kind < 2
+        self._p = photon_kv_pages(_ptr(k), _ptr(v), _ptr(k_scale), _ptr(v_scale), *st[:3], *ss, kind, *(
+            self.pages, self.page_rows, self.heads, self.head_dim))
+        self._ref = ctypes.addressof(self._p)
+
+    @classmethod
+    def alloc(cls, pages: int, page_rows: int, heads: int, head_dim: int, dtype, device="cuda") -> "KVPages":
+        """A zeroed pool laid out [pages, heads, page_rows, head_dim]."""
+        import torch
+        k, v = (torch.zeros(pages, heads, page_rows, head_dim, dtype=dtype, device=device) for _ in range(2))
+        if dtype.itemsize > 1:
+            return cls(k, v)
+        return cls(k, v, *(torch.zeros(pages, heads, page_rows, device=device) for _ in range(2)))
+
+    def _need(self, t, name: str) -> int:
+        code = _code(t, name)
+        if self._wide and t.dtype != self.dtype:
+            raise ValueError(f"{name}: expected {self.dtype}, as the pages, got {t.dtype}")
+        return code
+
+
+def _table(pages: KVPages, table) -> tuple:
+    import torch
+    if not isinstance(pages, KVPages):
+        raise TypeError(f"pages: expected KVPages, got {type(pages).__name__}")
+    if not isinstance(table, torch.Tensor) or table.dtype != torch.int32 or table.dim() != 2:
+        raise ValueError("table: expected int32 [sequences, pages of each]")
+    seqs, width = table.shape
+    if table.stride(1) != 1 and width > 1:
+        raise ValueError("table: the last dimension must be contiguous")
+    return seqs, width
+
+
+def rope(rope: Rope, pos, x, out, x2=None, out2=None, backward: bool = False, stream=None) -> None:
+    """photon_rope: x, out [tokens, heads, head_dim] (any strides, last dimension contiguous)
+    at positions pos (int32 [tokens]); x2, out2: a second tensor of the same tokens (q and
+    k in one launch).  out may be x.  backward: the gradient of x from that of out."""
+    import torch
+    if not isinstance(rope, Rope):
+        raise TypeError(f"rope: expected Rope, got {type(rope).__name__}")
+    code = _code(x, "x")
+    if x.dim() != 3:
+        raise ValueError("x: expected [tokens, heads, head_dim]")
+    n, heads, dim = x.shape
+    a, b = _rows(x, x.dtype, x.shape, "x"), _rows(out, x.dtype, x.shape, "out", out=True)
+    heads2, a2, b2 = 0, (0, 0), (0, 0)
+    if x2 is not None:
+        if not isinstance(x2, torch.Tensor) or x2.dim() != 3:
+            raise ValueError("x2: expected [tokens, heads, head_dim]")
+        heads2 = x2.shape[1]
+        a2, b2 = _rows(x2, x.dtype, (n, heads2, dim), "x2"), _rows(out2, x.dtype, (n, heads2, dim), "out2", out=True)
+    elif out2 is not None:
+        raise ValueError("out2 without x2")
+    _need(pos, torch.int32, n, "pos")
+    _launch(load_library().photon_rope, (x, out, x2, out2, pos, rope.freq), stream,
+            (code, rope._ref, pos.data_ptr(), n, dim, x.data_ptr(), a[0], a[1], heads, out.data_ptr(), b[0], b[1],
+             _ptr(x2), a2[0], a2[1], heads2, _ptr(out2), b2[0], b2[1], int(backward)))
+
+
+def _places(pages, table, pos, seq, k, v, out: bool, err) -> tuple:
+    import torch
+    seqs, width = _table(pages, table)
+    code = pages._need(k, "k")
+    n = pos.shape[0] if isinstance(pos, torch.Tensor) and pos.dim() == 1 else -1
+    if n < 0:
+        raise ValueError("pos: expected int32 [tokens]")
+    shape = (n, pages.heads, pages.head_dim)
+    a, b = _rows(k, k.dtype, shape, "k", out), _rows(v, k.dtype, shape, "v", out)
+    _need(pos, torch.int32, n, "pos")
+    if seq is not None:
+        _need(seq, torch.int32, n, "seq")
+    if err is not None:
+        _need(err, torch.int32, 1, "err")
+    return (pages._ref, code, table.data_ptr(), table.stride(0), seqs, width, _ptr(seq), pos.data_ptr(), n,
+            k.data_ptr(), a[0], a[1], v.data_ptr(), b[0], b[1])
+
+
+def kv_write(pages: KVPages, table, pos, k, v, seq=None, rope: Rope = None, q=None, q_out=None, stream=None,
+             err=None) -> None:
+    """photon_kv_write: stores k, v [tokens, heads, head_dim] at position pos[t] (int32; negative:
+    padding, left out) of sequence seq[t] (int32; None: t) through the block table (int32
+    [sequences, pages of each]).  rope: rotates k on the way, and q [tokens, q_heads,
+    head_dim] into q_out (may be q).  err: optional int32 CUDA tensor that receives a
+    nonzero code when a place does not exist."""
+    args = _places(pages, table, pos, seq, k, v, False, err)
+    heads, a, b = 0, (0, 0), (0, 0)
+    if rope is not None and not isinstance(rope, Rope):
+        raise TypeError(f"rope: expected Rope, got {type(rope).__name__}")
+    if q is not None:
+        if rope is None:
+            raise ValueError("q is rotated, so it needs rope")
+        if q.dim() != 3:
+            raise ValueError("q: expected [tokens, heads, head_dim]")
+        heads = q.shape[1]
+        shape = (k.shape[0], heads, pages.head_dim)
+        a, b = _rows(q, k.dtype, shape, "q"), _rows(q_out, k.dtype, shape, "q_out", out=True)
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    _launch(load_library().photon_kv_write,
+            (pages.k, table, pos, seq, k, v, q, q_out, None if rope is None else rope.freq, err), stream,
+            args + (None if rope is None else rope._ref, _ptr(q), a[0], a[1], heads, _ptr(q_out), b[0], b[1], _ptr(err)))
+
+
+def kv_read(pages: KVPages, table, pos, k, v, seq=None, stream=None, err=None) -> None:
+    """photon_kv_read: copies the places kv_write would write into k, v [tokens, heads,
+    head_dim] (code * scale of an 8-bit cache); rows of padding tokens are left as they were."""
+    args = _places(pages, table, pos, seq, k, v, True, err)
+    _launch(load_library().photon_kv_read, (pages.k, table, pos, seq, k, v, err), stream, args + (_ptr(err),))
+
+
+def attn_decode_paged(pages: KVPages, table, lens, q, out, window: int = 0, scale: Optional[float] = None, lse=None,
+                      stream=None, err=None) -> None:
+    """photon_attn_decode_paged: q, out [sequences, q_heads, head_dim], one new token per
+    sequence, over the lens[b] (int32) positions of sequence b (the last `window` of them
+    if given).  scale defaults to head_dim ** -0.5; lse: optional fp32 [sequences, q_heads]
+    log-sum-exp of the scaled scores, for joining with attention over other keys."""
+    import torch
+    seqs, width = _table(pages, table)
+    code = pages._need(q, "q")
+    if q.dim() != 3:
+        raise ValueError("q: expected [sequences, q_heads, head_dim]")
+    heads = q.shape[1]
+    shape = (seqs, heads, pages.head_dim)
+    a, b = _rows(q, q.dtype, shape, "q"), _rows(out, q.dtype, shape, "out", out=True)
+    _need(lens, torch.int32, seqs, "lens")
+    if lse is not None:
+        _need(lse, torch.float32, seqs * heads, "lse")
+    if err is not None:
+        _need(err, torch.int32, 1, "err")
+    _launch(load_library().photon_attn_decode_paged, (pages.k, table, lens, q, out, lse, err), stream,
+            (pages._ref, code, table.data_ptr(), table.stride(0), seqs, width, lens.data_ptr(), q.data_ptr(), a[0],
+             a[1], heads, int(window), pages.head_dim ** -0.5 if scale is None else float(scale), out.data_ptr(), b[0],
+             b[1], _ptr(lse), _ptr(err)))
 
 
 def debug_fail_alloc(n: int) -> None:

@@ -39,6 +39,8 @@ enum DeviceError : int {
   DEV_WAIT_TIMEOUT_EPILOGUE = 3,
   DEV_WAIT_TIMEOUT_BULK = 4,
   DEV_BAD_TOKEN = 5,
+  DEV_BAD_PLACE = 6,   // paged-cache operators: sequence, position or page out of range
+  DEV_BAD_LENGTH = 7,  // paged attention: length outside the block table
 };
 
 __device__ __forceinline__ void report_error(int* err, int code) {

@@ -342,6 +342,68 @@ bool launch_attn_prefill_simt(int dt, const AttnArgs& a, cudaStream_t s);
 bool launch_attn_prefill_path(int dt, const AttnArgs& a, int path, float* part, size_t part_bytes, int* err,
                               cudaStream_t s);
 
+// ---- operators around a caller's paged KV cache (k_kv_pages.cu, k_attn_paged.cu) ----
+// n / d for 0 <= n < 2^31 by a multiplication (Granlund and Montgomery 1994,
+// figure 4.1, N = 32): q = (umulhi(n, mul) + n) >> shift.
+struct FastDiv {
+  uint32_t mul, shift, d;
+};
+inline FastDiv fast_div(uint32_t d) {
+  uint32_t l = 0;
+  while ((1ull << l) < d) ++l;
+  return {(uint32_t)(((1ull << 32) * ((1ull << l) - d)) / d + 1), l, d};
+}
+struct RopeArgs {
+  const unsigned long long* freq = nullptr;  // turns a position, 64-bit fractions
+  int rot = 0;
+  bool interleaved = false;
+  float scale = 1.f;
+};
+// One [tokens][heads][head_dim] tensor in and out (element strides).
+struct HeadsArgs {
+  const void* in = nullptr;
+  void* out = nullptr;
+  long long in_tok = 0, in_head = 0, out_tok = 0, out_head = 0;
+  int heads = 0;
+};
+struct KvPoolArgs {
+  void *k, *v;
+  float *k_scale, *v_scale;
+  long long page, head, row;                   // element strides
+  long long scale_page, scale_head, scale_row;  // scale strides
+  int kind, pages, rows, heads, dh;
+  FastDiv div;  // by rows
+};
+// Block table and the (sequence, position) of every token.
+struct KvPlaceArgs {
+  const int* table;
+  long long table_stride;
+  int seqs, width;
+  const int *seq, *pos;
+  int tokens;
+};
+struct PagedAttnArgs {
+  KvPoolArgs pool;
+  const int* table;
+  long long table_stride;
+  int seqs, width;
+  const int* len;
+  const void* q;
+  long long q_seq, q_head;
+  int q_heads, window;
+  float scale;
+  void* o;
+  long long o_seq, o_head;
+  float* lse;
+};
+void launch_rope(int dt, const RopeArgs& r, const int* pos, int tokens, int dh, const HeadsArgs& a,
+                 const HeadsArgs& b, bool backward, cudaStream_t s);
+void launch_kv_write(int dt, const KvPoolArgs& p, const KvPlaceArgs& pl, const HeadsArgs& k, const HeadsArgs& v,
+                     const RopeArgs* r, const HeadsArgs& q, int* err, cudaStream_t s);
+void launch_kv_read(int dt, const KvPoolArgs& p, const KvPlaceArgs& pl, const HeadsArgs& k, const HeadsArgs& v,
+                    int* err, cudaStream_t s);
+void launch_attn_paged(int dt, const PagedAttnArgs& a, int* err, cudaStream_t s);
+
 // ---- error message of the calling thread (read by photon_last_error) ----
 void set_error_message(const char* msg);
 

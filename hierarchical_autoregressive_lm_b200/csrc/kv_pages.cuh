@@ -1,0 +1,135 @@
+// Device helpers shared by the operators around a caller's paged KV cache:
+// rows of eight elements, the 8-bit codes, positions to places.
+#pragma once
+
+#include <cuda_fp8.h>
+
+#include "common.cuh"
+#include "kernels.h"
+
+namespace photon {
+
+__device__ __forceinline__ uint32_t div_fast(uint32_t n, const FastDiv& f) {
+  return (__umulhi(n, f.mul) + n) >> f.shift;
+}
+
+// Storage of a page element by kind (PHOTON_KV_*).
+struct e4m3 {
+  __nv_fp8_storage_t x;
+};
+template <typename C> struct KvKind;
+template <> struct KvKind<float> { static constexpr bool narrow = false; };
+template <> struct KvKind<bf16> { static constexpr bool narrow = false; };
+template <> struct KvKind<e4m3> {
+  static constexpr bool narrow = true;
+  static constexpr float top = 448.f;
+};
+template <> struct KvKind<int8_t> {
+  static constexpr bool narrow = true;
+  static constexpr float top = 127.f;
+};
+
+// Eight consecutive elements as fp32.  VEC: the address is aligned to the
+// eight elements (16 bytes for fp32, which takes two loads).
+template <bool VEC>
+__device__ __forceinline__ void load8(float (&v)[8], const float* p) {
+  if constexpr (VEC) {
+    const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
+    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = p[i];
+  }
+}
+__device__ __forceinline__ void unpack_bf16(float* v, uint32_t w) {
+  v[0] = __uint_as_float(w << 16);
+  v[1] = __uint_as_float(w & 0xffff0000u);
+}
+template <bool VEC>
+__device__ __forceinline__ void load8(float (&v)[8], const bf16* p) {
+  if constexpr (VEC) {
+    const uint4 a = *reinterpret_cast<const uint4*>(p);
+    unpack_bf16(v, a.x), unpack_bf16(v + 2, a.y), unpack_bf16(v + 4, a.z), unpack_bf16(v + 6, a.w);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = __bfloat162float(p[i]);
+  }
+}
+__device__ __forceinline__ void unpack4(float* v, uint32_t w, e4m3) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const __half2 h(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w >> (16 * i)), __NV_E4M3));
+    const float2 f = __half22float2(h);
+    v[2 * i] = f.x, v[2 * i + 1] = f.y;
+  }
+}
+__device__ __forceinline__ void unpack4(float* v, uint32_t w, int8_t) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = (float)(int8_t)(w >> (8 * i));
+}
+template <bool VEC>
+__device__ __forceinline__ void load8(float (&v)[8], const e4m3* p) {
+  const uint2 a = *reinterpret_cast<const uint2*>(p);
+  unpack4(v, a.x, e4m3{}), unpack4(v + 4, a.y, e4m3{});
+}
+template <bool VEC>
+__device__ __forceinline__ void load8(float (&v)[8], const int8_t* p) {
+  const uint2 a = *reinterpret_cast<const uint2*>(p);
+  unpack4(v, a.x, int8_t{}), unpack4(v + 4, a.y, int8_t{});
+}
+
+template <bool VEC>
+__device__ __forceinline__ void store8(float* p, const float (&v)[8]) {
+  if constexpr (VEC) {
+    reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
+    reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) p[i] = v[i];
+  }
+}
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+template <bool VEC>
+__device__ __forceinline__ void store8(bf16* p, const float (&v)[8]) {
+  if constexpr (VEC) {
+    *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]),
+                                              pack_bf16(v[6], v[7]));
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) p[i] = __float2bfloat16_rn(v[i]);
+  }
+}
+// Values already multiplied by top / amax: rounded to nearest, ties to even.
+template <bool VEC>
+__device__ __forceinline__ void store8(e4m3* p, const float (&v)[8]) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    w[i] = __nv_cvt_float2_to_fp8x2(make_float2(v[2 * i], v[2 * i + 1]), __NV_SATFINITE, __NV_E4M3);
+  *reinterpret_cast<uint2*>(p) = make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
+}
+template <bool VEC>
+__device__ __forceinline__ void store8(int8_t* p, const float (&v)[8]) {
+  uint32_t w[2] = {0, 0};
+#pragma unroll
+  for (int i = 0; i < 8; ++i) w[i / 4] |= (uint32_t)(uint8_t)(int8_t)__float2int_rn(v[i]) << (8 * (i % 4));
+  *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+}
+
+// Page and row of position `pos` of a sequence; false where there is none
+// (reported, so that nothing is read or written for it).
+__device__ __forceinline__ bool page_of(const int* table, int width, const KvPoolArgs& p, int pos, int* page, int* row,
+                                        int* err) {
+  const uint32_t n = div_fast((uint32_t)pos, p.div);
+  if (n >= (uint32_t)width) return report_error(err, DEV_BAD_PLACE), false;
+  const int id = table[n];
+  if ((uint32_t)id >= (uint32_t)p.pages) return report_error(err, DEV_BAD_PLACE), false;
+  *page = id;
+  *row = pos - (int)n * p.rows;
+  return true;
+}
+
+}  // namespace photon

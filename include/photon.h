@@ -624,6 +624,140 @@ PHOTON_API int photon_vanilla_cache_info(photon_vanilla_cache* c, photon_vanilla
 /* Stream-ordered release (as photon_free_cache).  Errors: ERR_ARG, ERR_CUDA. */
 PHOTON_API int photon_vanilla_free_cache(photon_vanilla_cache* c);
 
+/* ------------------------------------------------------------------------
+ * Operators around a paged key-value cache, for callers that run their own
+ * layers next to the library's models: rotary positions, the cache write
+ * (optionally narrowing to 8 bits), the read back, and the attention of one
+ * new token per sequence.  None of them has a counterpart in the PHOTON
+ * paper.  All are asynchronous on `stream`, run on the current device (every
+ * pointer must be accessible there), keep nothing between calls, and may be
+ * captured into CUDA graphs.  dtype is the type of x, q, k, v and o: 0 fp32,
+ * 1 bf16.  Strides count elements, the last dimension is contiguous, and a
+ * stride may be anything that keeps distinct output elements apart. */
+
+/* Rotary positions.  Pair i (0 <= i < rot_dim/2) of a head turns by the
+ * angle p * f_i at position p: (a, b) -> scale * (a cos - b sin, a sin + b
+ * cos), where (a, b) are elements (i, i + rot_dim/2) of the head, or (2i, 2i
+ * + 1) when interleaved; elements from rot_dim on pass through.  f_i =
+ * theta^(-2i/rot_dim), changed for contexts longer than the trained one:
+ *   LINEAR: f_i / factor.
+ *   NTK:    theta * factor^(rot_dim / (rot_dim - 2)) in place of theta.
+ *   YARN:   (NTK-by-parts, arXiv 2309.00071 section 3.2) f_i * g + f_i /
+ *           factor * (1 - g) with g = (r - alpha) / (beta - alpha) clamped to
+ *           [0, 1] and r = original_len * f_i / (2 pi), the turns of the
+ *           pair within the trained length.
+ * scale is attn_scale if that is not 0, else 0.1 ln(factor) + 1 for YARN
+ * (section 3.4) and 1 otherwise. */
+enum { PHOTON_ROPE_PLAIN = 0, PHOTON_ROPE_LINEAR = 1, PHOTON_ROPE_NTK = 2, PHOTON_ROPE_YARN = 3 };
+typedef struct photon_rope_config {
+  int32_t rot_dim;      /* even, 2..512 (NTK: at least 4) */
+  int32_t scaling;      /* PHOTON_ROPE_* */
+  int32_t original_len; /* YARN: trained context length */
+  double theta, factor, alpha, beta, attn_scale;
+} photon_rope_config;
+
+/* Frequencies of a configuration, on the host (no device is touched):
+ * h_freq[i] = f_i / (2 pi) turns a position as a 64-bit binary fraction,
+ * round(2^64 * f_i / (2 pi)) modulo 2^64.  The kernels multiply it by the
+ * position modulo 2^64, which drops whole turns exactly, so an angle is as
+ * accurate at position 2^30 as at 1.  *h_scale receives the scale above.
+ * Errors: ERR_ARG. */
+PHOTON_API int photon_rope_frequencies(const photon_rope_config* cfg, uint64_t* h_freq, float* h_scale);
+
+/* The rotation as the kernels take it: d_freq is a device copy of h_freq. */
+typedef struct photon_rope_table {
+  const uint64_t* d_freq; /* [rot_dim / 2], 8-byte aligned */
+  int32_t rot_dim;
+  int32_t interleaved;
+  float scale;
+} photon_rope_table;
+
+/* y[n, h, :] = rotation of x[n, h, :] by position d_pos[n] (device int32,
+ * any sign) for n tokens and `heads` heads of even size head_dim >= rot_dim,
+ * at most 512.  x2 / y2 (heads2 heads, NULL and 0 for none) is a second tensor
+ * of the same tokens, for q and k in one launch.  backward != 0 applies the
+ * transposed map instead (the gradient of x from that of y).  y may be x (same
+ * strides); otherwise the outputs overlap no input.  Angles are exact to
+ * fp32 rounding, the arithmetic is fp32, the result is rounded once.
+ * tokens = 0 is a no-op.  Errors: ERR_ARG, ERR_CUDA. */
+PHOTON_API int photon_rope(int32_t dtype, const photon_rope_table* rope, const int32_t* d_pos, int32_t tokens,
+                           int32_t head_dim, const void* d_x, int64_t x_token, int64_t x_head, int32_t heads,
+                           void* d_y, int64_t y_token, int64_t y_head, const void* d_x2, int64_t x2_token,
+                           int64_t x2_head, int32_t heads2, void* d_y2, int64_t y2_token, int64_t y2_head,
+                           int32_t backward, void* stream);
+
+/* A pool of key and value pages of one layer, owned by the caller:
+ * element (page, head, row, e) of K and of V sits at page * page_stride +
+ * head * head_stride + row * row_stride + e, so that both [pages][heads]
+ * [page_rows][head_dim] and [pages][page_rows][heads][head_dim] fit.  Bases
+ * and strides are multiples of 16 bytes.  A narrow kind holds one fp32 scale
+ * per (page, head, row) of K and of V beside its codes; an element's value
+ * is code * scale. */
+enum { PHOTON_KV_F32 = 0, PHOTON_KV_BF16 = 1, PHOTON_KV_E4M3 = 2, PHOTON_KV_INT8 = 3 };
+typedef struct photon_kv_pages {
+  void* k;
+  void* v;
+  float* k_scale; /* NULL for F32 and BF16 */
+  float* v_scale;
+  int64_t page_stride, head_stride, row_stride;   /* of K and V, in elements */
+  int64_t scale_page, scale_head, scale_row;      /* of both scales, in floats */
+  int32_t kind;                                   /* PHOTON_KV_*; F32 with dtype 0 and BF16 with dtype 1 only */
+  int32_t pages, page_rows, heads, head_dim;      /* head_dim 32, 64, 128 or 256; page_rows >= 1 */
+} photon_kv_pages;
+
+/* Where positions live: d_table [seqs][width] (device int32, rows
+ * table_stride apart) names the page of positions r * page_rows .. of each
+ * sequence.  Entries past a sequence's positions are never read.  width *
+ * page_rows and tokens * heads are below 2^31.  A sequence index, position or
+ * page outside its range is left out (nothing is read or written for it) and
+ * reported in the error word d_err (device int32, nullable; zeroed by the
+ * caller, set to a nonzero code by the kernels).
+ *
+ * photon_kv_write stores token t (k and v rows [heads][head_dim]) at position
+ * d_pos[t] of sequence d_seq[t] (NULL: sequence t).  A negative position marks
+ * padding: the token is left out.  The places of one call must be distinct (a
+ * place named twice holds a mixture of the rows).  With `rope`, k is rotated
+ * by its position first, in fp32, and q (q_heads heads, NULL and 0 for none)
+ * is rotated into q_out (which may be q) in the same launch; q rows of padding
+ * tokens are left as they were.  A narrow cache row gets the scale s =
+ * max(amax, 1e-30) / top with amax its largest magnitude and top = 448 (E4M3)
+ * or 127 (INT8), and the codes round(x * (top / max(amax, 1e-30))), to nearest
+ * with ties to even; a row that holds an infinity or a NaN reads back as NaN
+ * (s = NaN, codes 0).  tokens = 0 is a no-op.
+ *
+ * photon_kv_read copies the same places out into k and v rows: the fp32
+ * product code * scale, rounded to dtype.  Rows of padding tokens are left as they were.  A
+ * place may be named any number of times.
+ * Errors: ERR_ARG, ERR_CUDA. */
+PHOTON_API int photon_kv_write(const photon_kv_pages* pages, int32_t dtype, const int32_t* d_table,
+                               int64_t table_stride, int32_t seqs, int32_t width, const int32_t* d_seq,
+                               const int32_t* d_pos, int32_t tokens, const void* d_k, int64_t k_token,
+                               int64_t k_head, const void* d_v, int64_t v_token, int64_t v_head,
+                               const photon_rope_table* rope, const void* d_q, int64_t q_token, int64_t q_head,
+                               int32_t q_heads, void* d_q_out, int64_t qo_token, int64_t qo_head,
+                               int32_t* d_err, void* stream);
+PHOTON_API int photon_kv_read(const photon_kv_pages* pages, int32_t dtype, const int32_t* d_table,
+                              int64_t table_stride, int32_t seqs, int32_t width, const int32_t* d_seq,
+                              const int32_t* d_pos, int32_t tokens, void* d_k, int64_t k_token, int64_t k_head,
+                              void* d_v, int64_t v_token, int64_t v_head, int32_t* d_err, void* stream);
+
+/* Attention of one new token per sequence over its pages.  Sequence b holds
+ * d_len[b] positions, the new token's own among them; query head h reads key
+ * head h / (q_heads / heads) (q_heads a multiple of heads) over positions t
+ * with max(0, len - window) <= t < len (window 0: all):
+ *   o[b, h, :] = sum_t softmax_t(scale * q . k_t) v_t,
+ *   d_lse[b, h] = ln sum_t exp(scale * q . k_t)   (fp32 [seqs, q_heads], nullable).
+ * A sequence without positions (length 0) gets o = 0 and lse = -infinity.
+ * A length outside 0 .. width * page_rows is clamped to it and reported in
+ * d_err, a page outside the pool leaves its positions out and is reported.
+ * Softmax statistics and sums are fp32.  Allocates the scratch of its split
+ * internally, as photon_attn_decode.  Errors: ERR_ARG, ERR_OOM, ERR_CUDA. */
+PHOTON_API int photon_attn_decode_paged(const photon_kv_pages* pages, int32_t dtype, const int32_t* d_table,
+                                        int64_t table_stride, int32_t seqs, int32_t width, const int32_t* d_len,
+                                        const void* d_q, int64_t q_seq, int64_t q_head, int32_t q_heads,
+                                        int32_t window, float scale, void* d_o, int64_t o_seq, int64_t o_head,
+                                        float* d_lse, int32_t* d_err, void* stream);
+
 /* Number of kernels this library has launched in this process so far
  * (every launch of every entry point; host-side counter, no GPU access). */
 PHOTON_API uint64_t photon_launch_count(void);

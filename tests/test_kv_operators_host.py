@@ -1,0 +1,188 @@
+"""Host-side checks of the paged-cache operators: frequencies and refusals, without a device.
+
+The entry points check every argument before any CUDA call, so a refused
+call needs no GPU; the addresses given here are never dereferenced.
+"""
+import ctypes
+from decimal import Decimal, getcontext
+
+import pytest
+import torch
+
+import hierarchical_autoregressive_lm_b200 as hal
+
+getcontext().prec = 60
+PI = Decimal("3.14159265358979323846264338327950288419716939937510582097494")
+A = 1 << 20  # an aligned address that nothing reads
+
+
+def _turns(rot, theta=10000.0, scaling="none", factor=1.0, original_len=0, alpha=1.0, beta=32.0):
+    """Turns a position of each pair in 60 digits."""
+    d, s, base = Decimal(rot), Decimal(factor), Decimal(theta)
+    if scaling == "ntk":
+        base *= s ** (d / (d - 2))
+    out = []
+    for i in range(rot // 2):
+        f = base ** (Decimal(-2 * i) / d)
+        if scaling == "linear":
+            f /= s
+        if scaling == "yarn":
+            g = (Decimal(original_len) * f / (2 * PI) - Decimal(alpha)) / (Decimal(beta) - Decimal(alpha))
+            g = min(Decimal(1), max(Decimal(0), g))
+            f = f * g + f / s * (1 - g)
+        out.append(f / (2 * PI) % 1)
+    return out
+
+
+@pytest.mark.parametrize("kw", [
+    dict(rot=64), dict(rot=2), dict(rot=128, theta=500000.0), dict(rot=64, scaling="linear", factor=4.0),
+    dict(rot=64, scaling="ntk", factor=8.0), dict(rot=128, scaling="yarn", factor=32.0, original_len=4096),
+    dict(rot=96, scaling="yarn", factor=2.5, original_len=2048, alpha=2.0, beta=16.0), dict(rot=4, theta=0.01)])
+def test_frequencies(kw):
+    kw = dict(kw)
+    rot = kw.pop("rot")
+    r = hal.Rope(rot, device="cpu", **kw)
+    want = _turns(rot, **kw)
+    assert len(r.turns) == rot // 2
+    for got, w in zip(r.turns, want):
+        # pow, the scaling's few operations and 1 / (2 pi), each within 2^-52 of its value, then 2^-65
+        off = abs(Decimal(got) / 2 ** 64 - w)
+        off = min(off, 1 - off)
+        size = max(w, Decimal(1) if kw.get("theta", 1e4) < 1 else w)  # below 1: whole turns were dropped from up to 1/theta
+        size *= 100 if kw.get("theta", 1e4) < 1 else 1
+        assert off <= size * 8 * Decimal(2) ** -52 + Decimal(2) ** -64, (got, w)
+    assert r.scale == pytest.approx(1 + 0.1 * float(Decimal(kw.get("factor", 1.0)).ln()) if kw.get("scaling") == "yarn" else 1.0, rel=1e-6)
+    assert hal.Rope(rot, device="cpu", attn_scale=0.75, **kw).scale == 0.75
+
+
+def test_rope_config_refusals():
+    for kw in (dict(rot_dim=3), dict(rot_dim=0), dict(rot_dim=514), dict(rot_dim=64, theta=0.0), dict(rot_dim=64, theta=float("nan")),
+               dict(rot_dim=64, scaling="linear", factor=0.5), dict(rot_dim=2, scaling="ntk", factor=2.0),
+               dict(rot_dim=64, scaling="yarn", factor=2.0), dict(rot_dim=64, scaling="yarn", factor=2.0, original_len=4, alpha=2.0, beta=2.0),
+               dict(rot_dim=64, attn_scale=float("inf")), dict(rot_dim=64, scaling="linear", factor=float("nan"))):
+        with pytest.raises(hal.PhotonError) as e:
+            hal.Rope(device="cpu", **kw)
+        assert e.value.code == -1
+    with pytest.raises(ValueError, match="scaling"):
+        hal.Rope(64, scaling="dynamic", device="cpu")
+    lib = hal.load_library()
+    assert lib.photon_rope_frequencies(None, None, None) == -1
+
+
+def _pages(**kw):
+    d = dict(k=A, v=A, k_scale=A, v_scale=A, page_stride=8 * 16 * 64, head_stride=16 * 64, row_stride=64, scale_page=8 * 16,
+             scale_head=16, scale_row=1, kind=2, pages=10, page_rows=16, heads=8, head_dim=64)
+    d.update(kw)
+    return hal.photon_kv_pages(**d)
+
+
+BAD_PAGES = [dict(kind=4), dict(kind=-1), dict(kind=0), dict(pages=0), dict(page_rows=0), dict(heads=0), dict(head_dim=48),
+             dict(k=None), dict(v=None), dict(k_scale=None), dict(v_scale=None), dict(k=A + 8), dict(page_stride=8 * 16 * 64 + 8),
+             dict(row_stride=72), dict(head_stride=-8), dict(k_scale=A + 2)]
+
+
+def _attn(lib, pages, **kw):
+    d = dict(dtype=1, table=A, stride=4, seqs=2, width=4, lens=A, q=A, q_heads=16, window=0, scale=0.125, o=A, lse=None)
+    d.update(kw)
+    return lib.photon_attn_decode_paged(None if pages is None else ctypes.byref(pages), d["dtype"], d["table"], d["stride"],
+                                        d["seqs"], d["width"], d["lens"], d["q"], 1024, 64, d["q_heads"], d["window"], d["scale"],
+                                        d["o"], 1024, 64, d["lse"], None, None)
+
+
+def test_attention_refusals():
+    lib = hal.load_library()
+    for kw in BAD_PAGES:
+        assert _attn(lib, _pages(**kw)) == -1, kw
+        assert lib.photon_last_error() != b""
+    for kw in (dict(dtype=2), dict(table=None), dict(seqs=-1), dict(width=0), dict(width=1 << 28), dict(lens=None), dict(q=None), dict(o=None),
+               dict(q_heads=12), dict(q_heads=0), dict(window=-1), dict(scale=float("nan")), dict(scale=float("inf")),
+               dict(q=A + 1), dict(lse=A + 2), dict(table=A + 1), dict(seqs=1 << 28)):
+        assert _attn(lib, _pages(), **kw) == -1, kw
+        assert lib.photon_last_error() != b""
+    assert _attn(lib, None) == -1
+    assert _attn(lib, _pages(), seqs=0, table=None) == 0  # nothing to do
+
+
+def test_write_and_read_refusals():
+    lib = hal.load_library()
+    rope = hal.photon_rope_table(A, 64, 0, 1.0)
+
+    def write(pages, **kw):
+        d = dict(dtype=1, table=A, seqs=2, width=4, seq=None, pos=A, tokens=2, k=A, v=A, rope=None, q=None, q_heads=0, q_out=None, qs=1024)
+        d.update(kw)
+        return lib.photon_kv_write(ctypes.byref(pages), d["dtype"], d["table"], 4, d["seqs"], d["width"], d["seq"], d["pos"], d["tokens"],
+                                   d["k"], 512, 64, d["v"], 512, 64, None if d["rope"] is None else ctypes.byref(d["rope"]),
+                                   d["q"], d["qs"], 64, d["q_heads"], d["q_out"], 1024, 64, None, None)
+
+    def read(pages, **kw):
+        d = dict(dtype=1, table=A, seqs=2, width=4, seq=None, pos=A, tokens=2, k=A, v=A)
+        d.update(kw)
+        return lib.photon_kv_read(ctypes.byref(pages), d["dtype"], d["table"], 4, d["seqs"], d["width"], d["seq"], d["pos"], d["tokens"],
+                                  d["k"], 512, 64, d["v"], 512, 64, None, None)
+
+    for f in (write, read):
+        for kw in BAD_PAGES:
+            assert f(_pages(**kw)) == -1, kw
+        for kw in (dict(dtype=3), dict(table=None), dict(seqs=0), dict(width=-1), dict(pos=None), dict(tokens=-1), dict(k=None), dict(v=None),
+                   dict(tokens=1 << 29), dict(pos=A + 1), dict(seq=A + 2), dict(k=A + 1)):
+            assert f(_pages(), **kw) == -1, (f, kw)
+            assert lib.photon_last_error() != b""
+        assert f(_pages(), tokens=0, pos=None, k=None, v=None, table=None) == 0
+    for kw in (dict(rope=hal.photon_rope_table(None, 64, 0, 1.0)), dict(rope=hal.photon_rope_table(A, 66, 0, 1.0)),
+               dict(rope=hal.photon_rope_table(A, 31, 0, 1.0)), dict(q=A, q_out=A, q_heads=16), dict(rope=rope, q_heads=16, q=A),
+               dict(rope=rope, q_heads=16, q_out=A), dict(rope=rope, q_heads=-1), dict(rope=rope, q=A, q_out=A, q_heads=16, qs=2048)):
+        assert write(_pages(), **kw) == -1, kw
+
+
+def test_rope_refusals():
+    lib = hal.load_library()
+    table = hal.photon_rope_table(A, 64, 0, 1.0)
+
+    def rope(t=table, **kw):
+        d = dict(dtype=0, pos=A, tokens=3, dim=64, x=A, heads=2, y=A, ys=128, x2=None, heads2=0, y2=None)
+        d.update(kw)
+        return lib.photon_rope(d["dtype"], None if t is None else ctypes.byref(t), d["pos"], d["tokens"], d["dim"], d["x"], 128, 64,
+                               d["heads"], d["y"], d["ys"], 64, d["x2"], 128, 64, d["heads2"], d["y2"], 128, 64, 0, None)
+
+    for kw in (dict(dtype=7), dict(pos=None), dict(tokens=-1), dict(dim=62), dict(dim=65), dict(dim=514), dict(x=None), dict(y=None),
+               dict(heads=0), dict(heads2=-1), dict(heads2=2), dict(heads2=2, x2=A), dict(ys=256), dict(x=A + 2), dict(tokens=1 << 30),
+               dict(t=None), dict(t=hal.photon_rope_table(A + 4, 64, 0, 1.0))):
+        assert rope(**kw) == -1, kw
+        assert lib.photon_last_error() != b""
+    assert rope(tokens=0, pos=None, x=None, y=None) == 0
+
+
+def test_struct_layouts():
+    assert ctypes.sizeof(hal.photon_kv_pages) == 4 * 8 + 6 * 8 + 5 * 4 + 4
+    assert ctypes.sizeof(hal.photon_rope_table) == 8 + 3 * 4 + 4
+    assert ctypes.sizeof(hal.photon_rope_config) == 3 * 4 + 4 + 5 * 8
+
+
+def test_binding_refuses_before_the_library():
+    k = torch.zeros(4, 2, 16, 64)
+    with pytest.raises(ValueError, match="CUDA"):
+        hal.KVPages(k, k)
+    with pytest.raises(ValueError, match="8-bit"):
+        hal.KVPages(k.to(torch.int8), k.to(torch.int8))
+    with pytest.raises(ValueError, match="8-bit"):
+        hal.KVPages(k, k, torch.zeros(4, 2, 16), torch.zeros(4, 2, 16))
+    with pytest.raises(ValueError, match="pages, heads"):
+        hal.KVPages(k.half(), k.half())
+    with pytest.raises(ValueError, match="of shape"):
+        hal.KVPages(k, k[:3])
+    with pytest.raises(ValueError, match="last dimension"):
+        hal.KVPages(k.transpose(2, 3), k.transpose(2, 3))
+    with pytest.raises(ValueError, match="expanded"):
+        hal.KVPages(k[:1].expand(4, 2, 16, 64), k[:1].expand(4, 2, 16, 64))
+    with pytest.raises(TypeError, match="KVPages"):
+        hal.attn_decode_paged(k, torch.zeros(1, 1, dtype=torch.int32), None, None, None)
+    r = hal.Rope(64, device="cpu")
+    x, pos = torch.zeros(3, 2, 64), torch.zeros(3, dtype=torch.int32)
+    with pytest.raises(ValueError, match="CUDA"):
+        hal.rope(r, pos, x, x)
+    with pytest.raises(ValueError, match="float32 or"):
+        hal.rope(r, pos, x.half(), x.half())
+    with pytest.raises(ValueError, match="tokens, heads"):
+        hal.rope(r, pos, x[0], x[0])
+    with pytest.raises(TypeError, match="Rope"):
+        hal.rope(None, pos, x, x)
