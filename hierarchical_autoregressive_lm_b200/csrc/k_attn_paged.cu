@@ -6,23 +6,409 @@
 // accumulator in fp32 and multiplies the two by 2^(m_old - m_new) when m
 // grows.
 //
-// One CTA of four warps per (sequence, key head, up to GH of its query
-// heads).  The warps take tiles of 16 positions in turn; their results are
-// joined in shared memory.
+// A unit is (sequence, key head, up to eight of its query heads); its
+// positions are cut into steps.  The rows of a page are read once for all
+// heads of a unit, so the kernel is bound by the cache's bytes; 4 flops per
+// element and head are far below what the tensor cores take.
+//
+// Split.  Lengths live on the device, so the host cannot deal them out.  One
+// CTA per resident slot takes an equal share of all steps of all units, in
+// unit order, from a prefix sum over the lengths: every CTA reads the same
+// number of rows, however uneven the sequences.  A unit that falls into
+// several CTAs leaves parts (accumulator, maximum, sum), which a second
+// kernel joins in the order of the positions.  Calls with few steps or many
+// units run one CTA per unit instead, without parts.
 #include <cmath>
+#include <type_traits>
 
 #include "kv_pages.cuh"
 #include "launch.cuh"
+#include "ptx_sm100.cuh"
 
 namespace photon {
 
 namespace {
 
 constexpr int kWarps = 4;
-constexpr int kTile = 16;  // positions a warp takes at a time
+constexpr int kThreads = 32 * kWarps;
+constexpr int kHeadsMax = 8;  // query heads of a unit
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+
+// How a launch deals out its work; parts are [cta][2][kHeadsMax].
+struct Plan {
+  int chunks, gh;  // units per key head, query heads of each
+  int ctas;        // 0: one CTA per unit
+  int min_steps;   // least steps worth a CTA
+  float* acc;      // [cta][2][kHeadsMax][D]
+  float2* ml;      // maximum and sum
+  int4* meta;      // [cta]: sequence, unit within it, last CTA of the unit that starts here (-1: none)
+};
+
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool valid) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp4(uint32_t dst, const void* src, bool valid) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(valid ? 4 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void ldsm(uint32_t (&r)[4], uint32_t a) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a) : "memory");
+}
+__device__ __forceinline__ void ldsm_t(uint32_t (&r)[4], uint32_t a) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a) : "memory");
+}
+// c[16 x 8] += a[16 x 16] b[16 x 8], fp32 accumulators.
+__device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                    uint32_t b1, bf16) {
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+               : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3]) : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                    uint32_t b1, __half) {
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+               : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3]) : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// Codes (four bytes) as fp16 pairs of bytes 0, 1 and 2, 3: exact.
+__device__ __forceinline__ void codes_f16(uint32_t& lo, uint32_t& hi, uint32_t w, e4m3) {
+  asm("{ .reg .b16 a, b; mov.b32 {a, b}, %2; cvt.rn.f16x2.e4m3x2 %0, a; cvt.rn.f16x2.e4m3x2 %1, b; }"
+      : "=r"(lo), "=r"(hi) : "r"(w));
+}
+__device__ __forceinline__ void codes_f16(uint32_t& lo, uint32_t& hi, uint32_t w, int8_t) {
+  // code + 128 in the low bits of 1024
+  w ^= 0x80808080u;
+  const uint32_t a = __byte_perm(w, 0x64646464u, 0x4140), b = __byte_perm(w, 0x64646464u, 0x4342);
+  const __half2 c = __floats2half2_rn(1152.f, 1152.f);
+  const __half2 x = __hsub2(*reinterpret_cast<const __half2*>(&a), c), y = __hsub2(*reinterpret_cast<const __half2*>(&b), c);
+  lo = *reinterpret_cast<const uint32_t*>(&x), hi = *reinterpret_cast<const uint32_t*>(&y);
+}
+// Codes as bf16 pairs of bytes 0, 2 and 1, 3: exact.
+__device__ __forceinline__ void codes_bf16(uint32_t& even, uint32_t& odd, uint32_t w, e4m3) {
+  uint32_t a, b;
+  codes_f16(a, b, __byte_perm(w, 0, 0x3120), e4m3{});
+  const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&a)), y = __half22float2(*reinterpret_cast<const __half2*>(&b));
+  even = pack_bf16(x.x, x.y), odd = pack_bf16(y.x, y.y);
+}
+__device__ __forceinline__ void codes_bf16(uint32_t& even, uint32_t& odd, uint32_t w, int8_t) {
+  // code + 128 in the low bits of 2^23
+  w ^= 0x80808080u;
+  float f[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) f[i] = __uint_as_float(__byte_perm(w, 0x4b000000u, 0x7440 + i)) - 8388736.f;
+  even = pack_bf16(f[0], f[2]), odd = pack_bf16(f[1], f[3]);
+}
+
+// What a unit's positions are.
+struct Unit {
+  int b, kh, h0, nh;  // sequence, key head, first query head and their number
+  int first, len;     // positions first .. len - 1
+  const int* table;
+};
+
+// Results of the warps over their positions, before they are joined.
+template <int D>
+struct Joint {
+  static constexpr int kPitch = D + 8;
+  float o[kWarps][kHeadsMax][kPitch];
+  float m[kWarps][kHeadsMax], l[kWarps][kHeadsMax];
+};
+
+// bf16 queries on the tensor cores (m16n8k16: with eight query heads, one
+// token each, larger tiles would stay empty; the cache's bytes are the bound).
+//
+// A warp takes tiles of TP positions through a ring of cp.async stages of its
+// own, so no barrier stands between load and use; ldmatrix reads the rows,
+// whose 16-byte chunks are permuted so that eight rows fall into different
+// banks.  The heads are rows 0-7 of the products' left side; rows 8-15 carry
+// what rounding leaves behind, at no cost:
+//  * weights go to the second product as the sum of two bf16 numbers, off by
+//    2^-17 (one bf16 would be off by 2^-9, as much as the result's own rounding);
+//  * over 8-bit pages the first product runs in fp16, which holds every code
+//    exactly; q is divided by the power of two at its largest element and what
+//    fp16 cannot hold of it follows times 2^24.
+// In the second product the codes are bf16 (exact too): a weight times a
+// scale has fp32's range, which fp16 has not.
+template <typename C, int D>
+struct TensorCores {
+  using T = bf16;
+  static constexpr int GH = kHeadsMax;
+  static constexpr bool kNarrow = KvKind<C>::narrow;
+  static constexpr int kRow = D * sizeof(C), kChunks = kRow / 16;
+  static constexpr int TP = 4096 / kRow < 16 ? 16 : 4096 / kRow > 64 ? 64 : 4096 / kRow;
+  static constexpr int kStep = kWarps * TP;
+  static constexpr int kTile = TP * kRow;  // bytes of K (and of V)
+  static constexpr int kMeta = 16 + (kNarrow ? 8 * TP : 0);
+  static constexpr int kStage = 2 * kTile + kMeta;
+  static constexpr int kStages = 24576 / (2 * kTile) < 3 ? 3 : 24576 / (2 * kTile) > 6 ? 6 : 24576 / (2 * kTile);
+  static constexpr int kWarpBytes = kStages * kStage;
+  static constexpr int kSmem = kWarps * kWarpBytes;
+  static constexpr int kCtas = 2 * kSmem <= 220 * 1024 ? 2 : 1;
+  static_assert(kSmem >= (int)sizeof(Joint<D>) && kTile % 128 == 0, "the ring is reused for the join");
+  static constexpr int KS = D / 16;   // k steps of the first product
+  static constexpr int NT = D / 8;    // column tiles of the second
+  static constexpr int SUB = TP / 16;
+  static constexpr int PL = (TP + 31) / 32;  // positions a lane looks up
+
+  // Byte of chunk c of row r of a tile.
+  static __device__ __forceinline__ uint32_t place(int r, int c) {
+    if constexpr (kChunks >= 8) {
+      return r * kRow + ((c ^ (r & 7)) << 4);
+    } else {
+      constexpr int RPL = 8 / kChunks;  // rows of a 128-byte line
+      const int line = r / RPL;
+      return line * 128 + ((((r % RPL) * kChunks + c) ^ (line & (kChunks - 1))) << 4);
+    }
+  }
+
+  static __device__ __forceinline__ void run(const PagedAttnArgs& a, const Unit& u, int p0, int p1, unsigned char* smem,
+                                             int* err) {
+    const KvPoolArgs& p = a.pool;
+    const int w = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const uint32_t ring = ptx::smem_u32(smem) + w * (kStages * 2 * kTile);
+    unsigned char* const metas = smem + kWarps * (kStages * 2 * kTile) + w * (kStages * kMeta);
+
+    // pages of this warp's tile i, and the copies of it
+    const int tiles = (p1 - p0 + TP - 1) / TP, mine = tiles > w ? (tiles - w + kWarps - 1) / kWarps : 0;
+    auto look_up = [&](int (&page)[PL], int i) {
+#pragma unroll
+      for (int j = 0; j < PL; ++j) {
+        const int pos = p0 + (w + i * kWarps) * TP + j * 32 + lane % TP;
+        page[j] = -1;
+        if (i < mine && pos < p1) {
+          page[j] = u.table[div_fast((uint32_t)pos, p.div)];
+          if ((uint32_t)page[j] >= (uint32_t)p.pages) report_error(err, DEV_BAD_PLACE), page[j] = -1;
+        }
+      }
+    };
+    auto issue = [&](const int (&page)[PL], int i) {
+      if (i < mine) {
+        const int st = i % kStages;
+        long long off[PL];
+        unsigned char* const meta = metas + st * kMeta;
+#pragma unroll
+        for (int j = 0; j < PL; ++j) {
+          const int pos = p0 + (w + i * kWarps) * TP + j * 32 + lane % TP;
+          const int row = pos - (int)div_fast((uint32_t)pos, p.div) * p.rows;
+          const bool ok = page[j] >= 0;
+          off[j] = ok ? page[j] * p.page + row * p.row + u.kh * p.head : -1;
+          const unsigned mask = __ballot_sync(0xffffffffu, ok);
+          if (lane == 0) reinterpret_cast<unsigned*>(meta)[j] = mask;
+          if (kNarrow && lane < TP) {
+            const long long s = ok ? page[j] * p.scale_page + row * p.scale_row + u.kh * p.scale_head : 0;
+            const uint32_t dst = ptx::smem_u32(meta + 16) + (j * 32 + lane) * 4;
+            cp4(dst, p.k_scale + s, ok);
+            cp4(dst + 4 * TP, p.v_scale + s, ok);
+          }
+        }
+        const uint32_t dst = ring + st * 2 * kTile;
+#pragma unroll
+        for (int n = 0; n < TP * kChunks / 32; ++n) {
+          const int id = n * 32 + lane, r = id / kChunks, c = id % kChunks;
+          // all lanes of one copy read rows of the same half of the tile
+          const long long o = __shfl_sync(0xffffffffu, off[n * 32 / kChunks / 32], r % 32);
+          const long long e = (o < 0 ? 0 : o) + c * (16 / (int)sizeof(C));
+          cp16(dst + place(r, c), (const C*)p.k + e, o >= 0);
+          cp16(dst + kTile + place(r, c), (const C*)p.v + e, o >= 0);
+        }
+      }
+      cp_commit();
+    };
+
+    int page[PL];
+    {
+      int pages[kStages - 1][PL];
+#pragma unroll
+      for (int i = 0; i < kStages - 1; ++i) look_up(pages[i], i);
+#pragma unroll
+      for (int i = 0; i < kStages - 1; ++i) issue(pages[i], i);
+      look_up(page, kStages - 1);
+    }
+
+    // q: rows 0-7 of the left side, in the order of k that the codes come in
+    uint32_t qa[KS][kNarrow ? 4 : 2];
+    float to_log2 = a.scale * kLog2e;
+    {
+      const T* q = (const T*)a.q + u.b * a.q_seq + (u.h0 + g) * a.q_head;
+      const bool there = g < u.nh;
+      if constexpr (kNarrow) {
+        float x[KS][4];
+        uint32_t top = 0;
+#pragma unroll
+        for (int k = 0; k < KS; ++k)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            x[k][i] = there ? ld_f(q + 16 * k + 4 * t + i) : 0.f;
+            top = max(top, __float_as_uint(x[k][i]) & 0x7fffffffu);
+          }
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        const uint32_t e = min(max(top >> 23, 1u), 253u);
+        to_log2 *= __uint_as_float(e << 23);
+        const float down = __uint_as_float((254 - e) << 23);
+#pragma unroll
+        for (int k = 0; k < KS; ++k)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const float y = x[k][2 * i] * down, z = x[k][2 * i + 1] * down;
+            const __half2 h = __floats2half2_rn(y, z);
+            const float2 f = __half22float2(h);
+            const __half2 l = __floats2half2_rn(isfinite(y) ? (y - f.x) * 0x1p24f : 0.f, isfinite(z) ? (z - f.y) * 0x1p24f : 0.f);
+            qa[k][2 * i] = *reinterpret_cast<const uint32_t*>(&h);
+            qa[k][2 * i + 1] = *reinterpret_cast<const uint32_t*>(&l);
+          }
+      } else {
+#pragma unroll
+        for (int k = 0; k < KS; ++k)
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            qa[k][i] = there ? pack_bf16(ld_f(q + 16 * k + 8 * i + 2 * t), ld_f(q + 16 * k + 8 * i + 2 * t + 1)) : 0u;
+      }
+    }
+
+    float m = -INFINITY, l = 0.f, o[NT][4];
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) o[n][i] = 0.f;
+
+    for (int i = 0; i < mine; ++i) {
+      cp_wait<kStages - 2>();
+      __syncwarp();  // every lane's copies of tile i are here, and tile i - 1 has been read
+      issue(page, i + kStages - 1);
+      look_up(page, i + kStages);
+      const int st = i % kStages;
+      const uint32_t kt = ring + st * 2 * kTile, vt = kt + kTile;
+      const unsigned char* const meta = metas + st * kMeta;
+      const float* const scales = reinterpret_cast<const float*>(meta + 16);
+
+      // scores: head g, positions 16 u + 8 j + 2 t + {0, 1}
+      float s[SUB][2][2];
+#pragma unroll
+      for (int u16 = 0; u16 < SUB; ++u16) {
+        float c[2][4] = {};
+        const int r = u16 * 16 + (lane & 7) + (lane >> 4) * 8;
+#pragma unroll
+        for (int k = 0; k < KS; k += kNarrow ? 2 : 1) {
+          uint32_t x[4];
+          ldsm(x, kt + place(r, (kNarrow ? k : 2 * k) + ((lane >> 3) & 1)));
+          if constexpr (kNarrow) {
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+              for (int kk = 0; kk < 2; ++kk) {
+                uint32_t b0, b1;
+                codes_f16(b0, b1, x[2 * j + kk], C());
+                mma(c[j], qa[k + kk][0], qa[k + kk][1], qa[k + kk][2], qa[k + kk][3], b0, b1, __half());
+              }
+          } else {
+#pragma unroll
+            for (int j = 0; j < 2; ++j) mma(c[j], qa[k][0], 0u, qa[k][1], 0u, x[2 * j], x[2 * j + 1], bf16());
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          if constexpr (kNarrow) {
+            const float2 ks = *reinterpret_cast<const float2*>(scales + u16 * 16 + j * 8 + 2 * t);
+            s[u16][j][0] = (c[j][0] + c[j][2] * 0x1p-24f) * to_log2 * ks.x;
+            s[u16][j][1] = (c[j][1] + c[j][3] * 0x1p-24f) * to_log2 * ks.y;
+          } else {
+            s[u16][j][0] = c[j][0] * to_log2;
+            s[u16][j][1] = c[j][1] * to_log2;
+          }
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < PL; ++j) {
+        const unsigned mask = reinterpret_cast<const unsigned*>(meta)[j];
+        if (mask != 0xffffffffu) {
+#pragma unroll
+          for (int n = 0; n < (SUB < 2 ? SUB : 2) * 4; ++n) {
+            const int at = n / 4 * 16 + (n / 2 % 2) * 8 + 2 * t + n % 2;
+            if (!((mask >> at) & 1)) s[j * 2 + n / 4][n / 2 % 2][n % 2] = -INFINITY;
+          }
+        }
+      }
+      // softmax
+      float mx = -INFINITY;
+#pragma unroll
+      for (int n = 0; n < SUB * 4; ++n) mx = fmaxf(mx, s[n / 4][n / 2 % 2][n % 2]);
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+      mx = fmaxf(mx, m);
+      const float base = mx == -INFINITY ? 0.f : mx;
+      if (__any_sync(0xffffffffu, mx != m)) {
+        const float grow = exp2f(m - base);
+        l *= grow;
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) o[n][k] *= grow;
+      }
+      m = mx;
+#pragma unroll
+      for (int u16 = 0; u16 < SUB; ++u16) {
+        uint32_t pa[4];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          float x = exp2f(s[u16][j][0] - base), y = exp2f(s[u16][j][1] - base);
+          l += x + y;
+          if constexpr (kNarrow) {
+            const float2 vs = *reinterpret_cast<const float2*>(scales + TP + u16 * 16 + j * 8 + 2 * t);
+            x *= vs.x, y *= vs.y;
+          }
+          const uint32_t hi = pack_bf16(x, y);
+          pa[2 * j] = hi;
+          pa[2 * j + 1] = pack_bf16(x - __uint_as_float(hi << 16), y - __uint_as_float(hi & 0xffff0000u));
+        }
+        const int r = u16 * 16 + (lane & 15);
+#pragma unroll
+        for (int c = 0; c < kChunks; c += 2) {
+          uint32_t x[4];
+          ldsm_t(x, vt + place(r, c + (lane >> 4)));
+          if constexpr (kNarrow) {
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              uint32_t e0, e1, o0, o1;
+              codes_bf16(e0, o0, x[2 * j], C());
+              codes_bf16(e1, o1, x[2 * j + 1], C());
+              mma(o[2 * (c + j)], pa[0], pa[1], pa[2], pa[3], e0, e1, bf16());
+              mma(o[2 * (c + j) + 1], pa[0], pa[1], pa[2], pa[3], o0, o1, bf16());
+            }
+          } else {
+#pragma unroll
+            for (int j = 0; j < 2; ++j) mma(o[c + j], pa[0], pa[1], pa[2], pa[3], x[2 * j], x[2 * j + 1], bf16());
+          }
+        }
+      }
+    }
+    cp_wait<0>();
+    l += __shfl_xor_sync(0xffffffffu, l, 1);
+    l += __shfl_xor_sync(0xffffffffu, l, 2);
+    __syncthreads();  // all rings have been read
+    Joint<D>& joint = *reinterpret_cast<Joint<D>*>(smem);
+    float* const row = joint.o[w][g];
+    if (t == 0) joint.m[w][g] = m, joint.l[w][g] = l;
+    if constexpr (kNarrow) {
+#pragma unroll
+      for (int c = 0; c < NT / 2; ++c)
+        *reinterpret_cast<float4*>(row + 16 * c + 4 * t) = make_float4(o[2 * c][0] + o[2 * c][2], o[2 * c + 1][0] + o[2 * c + 1][2],
+                                                                       o[2 * c][1] + o[2 * c][3], o[2 * c + 1][1] + o[2 * c + 1][3]);
+    } else {
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+        *reinterpret_cast<float2*>(row + 8 * n + 2 * t) = make_float2(o[n][0] + o[n][2], o[n][1] + o[n][3]);
+    }
+    __syncthreads();
+  }
+};
 
 __device__ __forceinline__ float one_f(float x) { return x; }
-__device__ __forceinline__ float one_f(bf16 x) { return __bfloat162float(x); }
 __device__ __forceinline__ float one_f(int8_t x) { return (float)x; }
 __device__ __forceinline__ float one_f(e4m3 x) {
   return __half2float(__half(__nv_cvt_fp8_to_halfraw(x.x, __NV_E4M3)));
@@ -42,181 +428,396 @@ __device__ __forceinline__ void load_n(float (&v)[N], const C* p) {
   }
 }
 
-template <typename T, typename C, int D, int GH>
-__global__ void __launch_bounds__(kWarps * 32) k_attn_paged(const PagedAttnArgs a, const int chunks, int* err) {
-  constexpr int VPL = D / 32;  // output elements of a lane
-  __shared__ __align__(16) float sq[GH][D];
-  __shared__ __align__(16) float so[kWarps][GH][D];
-  __shared__ __align__(16) float sp[kWarps][kTile][GH];
-  __shared__ long long soff[kWarps][kTile];
-  __shared__ float sm[kWarps][GH], sl[kWarps][GH];
-  pdl_wait();
-  pdl_trigger();
-  const KvPoolArgs& p = a.pool;
-  const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
-  const int b = blockIdx.x / (p.heads * chunks), rest = blockIdx.x % (p.heads * chunks);
-  const int kh = rest / chunks, group = a.q_heads / p.heads;
-  const int h0 = kh * group + rest % chunks * GH, nh = min(GH, (kh + 1) * group - h0);
-  const int cap = a.width * p.rows;
-  int len = a.len[b];
-  if (len < 0 || len > cap) {
-    report_error(err, DEV_BAD_LENGTH);
-    len = len < 0 ? 0 : cap;
-  }
-  const int first = a.window > 0 ? max(0, len - a.window) : 0;
-  for (int i = tid; i < GH * D; i += kWarps * 32) {
-    const int h = i / D, e = i % D;
-    sq[h][e] = 0.f;
-    if (h < nh) sq[h][e] = ld_f((const T*)a.q + b * a.q_seq + (h0 + h) * a.q_head + e) * (a.scale * 1.4426950408889634f);
-  }
-  __syncthreads();
-  const int* table = a.table + b * a.table_stride;
-  float m[GH], l[GH], acc[GH][VPL];
-#pragma unroll
-  for (int h = 0; h < GH; ++h) {
-    m[h] = -INFINITY, l[h] = 0.f;
-#pragma unroll
-    for (int i = 0; i < VPL; ++i) acc[h][i] = 0.f;
-  }
-  for (int t0 = first + w * kTile; t0 < len; t0 += kWarps * kTile) {
-    // lanes 0..15 (and 16..31 again): place of one position, -1 where there is none
-    long long off = -1;
-    float ks = 1.f, vs = 1.f;
-    {
-      const int pos = t0 + lane % kTile;
-      int page, row;
-      if (pos < len && page_of(table, a.width, p, pos, &page, &row, err)) {
-        off = page * p.page + row * p.row + kh * p.head;
-        if constexpr (KvKind<C>::narrow) {
-          const long long s = page * p.scale_page + row * p.scale_row + kh * p.scale_head;
-          ks = p.k_scale[s], vs = p.v_scale[s];
-        }
-      }
-      if (lane < kTile) soff[w][lane] = off;
+// fp32 queries: everything in fp32, which the tensor cores do not multiply.
+// A warp takes tiles of 16 positions; lane (g, t) scores positions g and g +
+// 8 over every fourth group of eight elements, then sums D / 32 output
+// elements over the tile.
+template <typename C, int D, int GH_>
+struct CudaCores {
+  using T = float;
+  static constexpr int GH = GH_;
+  static constexpr int TP = 16, kStep = kWarps * TP;
+  static constexpr int VPL = D / 32;  // output elements of a lane
+  static constexpr int kCtas = 2;
+  struct Shared {
+    Joint<D> joint;
+    float q[GH][D];
+    float p[kWarps][TP][GH];
+    long long off[kWarps][TP];
+  };
+  static constexpr int kSmem = sizeof(Shared);
+
+  static __device__ __forceinline__ void run(const PagedAttnArgs& a, const Unit& u, int p0, int p1, unsigned char* smem,
+                                             int* err) {
+    Shared& sh = *reinterpret_cast<Shared*>(smem);
+    const KvPoolArgs& p = a.pool;
+    const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
+    for (int i = tid; i < GH * D; i += kThreads) {
+      const int h = i / D, e = i % D;
+      sh.q[h][e] = h < u.nh ? ((const T*)a.q)[u.b * a.q_seq + (u.h0 + h) * a.q_head + e] * (a.scale * kLog2e) : 0.f;
     }
-    __syncwarp();
-    // lane (g, t): positions g and g + 8, every fourth group of eight elements
-    float s[2][GH];
+    __syncthreads();
+    float m[GH], l[GH], acc[GH][VPL];
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      const long long o = soff[w][g + 8 * r];
+    for (int h = 0; h < GH; ++h) {
+      m[h] = -INFINITY, l[h] = 0.f;
 #pragma unroll
-      for (int h = 0; h < GH; ++h) s[r][h] = 0.f;
-      if (o >= 0) {
+      for (int i = 0; i < VPL; ++i) acc[h][i] = 0.f;
+    }
+    for (int t0 = p0 + w * TP; t0 < p1; t0 += kStep) {
+      // lanes 0..15 (and 16..31 again): place of one position, -1 where there is none
+      long long off = -1;
+      float ks = 1.f, vs = 1.f;
+      {
+        const int pos = t0 + lane % TP;
+        int page, row;
+        if (pos < p1 && page_of(u.table, a.width, p, pos, &page, &row, err)) {
+          off = page * p.page + row * p.row + u.kh * p.head;
+          if constexpr (KvKind<C>::narrow) {
+            const long long s = page * p.scale_page + row * p.scale_row + u.kh * p.scale_head;
+            ks = p.k_scale[s], vs = p.v_scale[s];
+          }
+        }
+        if (lane < TP) sh.off[w][lane] = off;
+      }
+      __syncwarp();
+      float s[2][GH];
 #pragma unroll
-        for (int i = 0; i < VPL; ++i) {
-          const int e = (t + 4 * i) * 8;
-          float x[8];
-          load8<true>(x, (const C*)p.k + o + e);
+      for (int r = 0; r < 2; ++r) {
+        const long long o = sh.off[w][g + 8 * r];
 #pragma unroll
-          for (int h = 0; h < GH; ++h) {
-            const float4 q0 = *reinterpret_cast<const float4*>(&sq[h][e]);
-            const float4 q1 = *reinterpret_cast<const float4*>(&sq[h][e + 4]);
-            s[r][h] += x[0] * q0.x + x[1] * q0.y + x[2] * q0.z + x[3] * q0.w + x[4] * q1.x + x[5] * q1.y +
-                       x[6] * q1.z + x[7] * q1.w;
+        for (int h = 0; h < GH; ++h) s[r][h] = 0.f;
+        if (o >= 0) {
+#pragma unroll
+          for (int i = 0; i < VPL; ++i) {
+            const int e = (t + 4 * i) * 8;
+            float x[8];
+            load8<true>(x, (const C*)p.k + o + e);
+#pragma unroll
+            for (int h = 0; h < GH; ++h) {
+              const float4 q0 = *reinterpret_cast<const float4*>(&sh.q[h][e]);
+              const float4 q1 = *reinterpret_cast<const float4*>(&sh.q[h][e + 4]);
+              s[r][h] += x[0] * q0.x + x[1] * q0.y + x[2] * q0.z + x[3] * q0.w + x[4] * q1.x + x[5] * q1.y +
+                         x[6] * q1.z + x[7] * q1.w;
+            }
           }
         }
       }
-    }
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      const bool seen = soff[w][g + 8 * r] >= 0;
-      const float k_scale = __shfl_sync(0xffffffffu, ks, g + 8 * r);
+      for (int r = 0; r < 2; ++r) {
+        const bool seen = sh.off[w][g + 8 * r] >= 0;
+        const float k_scale = __shfl_sync(0xffffffffu, ks, g + 8 * r);
+#pragma unroll
+        for (int h = 0; h < GH; ++h) {
+          s[r][h] += __shfl_xor_sync(0xffffffffu, s[r][h], 1);
+          s[r][h] += __shfl_xor_sync(0xffffffffu, s[r][h], 2);
+          s[r][h] = seen ? s[r][h] * k_scale : -INFINITY;
+        }
+      }
+      const float v0 = __shfl_sync(0xffffffffu, vs, g), v1 = __shfl_sync(0xffffffffu, vs, g + 8);
 #pragma unroll
       for (int h = 0; h < GH; ++h) {
-        s[r][h] += __shfl_xor_sync(0xffffffffu, s[r][h], 1);
-        s[r][h] += __shfl_xor_sync(0xffffffffu, s[r][h], 2);
-        s[r][h] = seen ? s[r][h] * k_scale : -INFINITY;
+        float mx = fmaxf(s[0][h], s[1][h]);
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+        mx = fmaxf(mx, m[h]);
+        const float base = mx == -INFINITY ? 0.f : mx, grow = exp2f(m[h] - base);
+        const float x = exp2f(s[0][h] - base), y = exp2f(s[1][h] - base);
+        m[h] = mx;
+        l[h] = l[h] * grow + (x + y);
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) acc[h][i] *= grow;
+        if (t == 0) sh.p[w][g][h] = x * v0, sh.p[w][g + 8][h] = y * v1;
       }
+      __syncwarp();
+#pragma unroll 4
+      for (int j = 0; j < TP; ++j) {
+        const long long o = sh.off[w][j];
+        if (o < 0) continue;
+        float x[VPL];
+        load_n<VPL>(x, (const C*)p.v + o + lane * VPL);
+#pragma unroll
+        for (int h = 0; h < GH; ++h)
+#pragma unroll
+          for (int i = 0; i < VPL; ++i) acc[h][i] += sh.p[w][j][h] * x[i];
+      }
+      __syncwarp();
     }
-    const float v0 = __shfl_sync(0xffffffffu, vs, g), v1 = __shfl_sync(0xffffffffu, vs, g + 8);
 #pragma unroll
     for (int h = 0; h < GH; ++h) {
-      float mx = fmaxf(s[0][h], s[1][h]);
 #pragma unroll
-      for (int o = 4; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-      mx = fmaxf(mx, m[h]);
-      const float base = mx == -INFINITY ? 0.f : mx, grow = exp2f(m[h] - base);
-      const float p0 = exp2f(s[0][h] - base), p1 = exp2f(s[1][h] - base);
-      m[h] = mx;
-      l[h] = l[h] * grow + (p0 + p1);
+      for (int o = 4; o < 32; o <<= 1) l[h] += __shfl_xor_sync(0xffffffffu, l[h], o);
+      if (lane == 0) sh.joint.m[w][h] = m[h], sh.joint.l[w][h] = l[h];
 #pragma unroll
-      for (int i = 0; i < VPL; ++i) acc[h][i] *= grow;
-      if (t == 0) sp[w][g][h] = p0 * v0, sp[w][g + 8][h] = p1 * v1;
+      for (int i = 0; i < VPL; ++i) sh.joint.o[w][h][lane * VPL + i] = acc[h][i];
     }
-    __syncwarp();
-#pragma unroll 4
-    for (int j = 0; j < kTile; ++j) {
-      const long long o = soff[w][j];
-      if (o < 0) continue;
-      float x[VPL];
-      load_n<VPL>(x, (const C*)p.v + o + lane * VPL);
-#pragma unroll
-      for (int h = 0; h < GH; ++h)
-#pragma unroll
-        for (int i = 0; i < VPL; ++i) acc[h][i] += sp[w][j][h] * x[i];
-    }
-    __syncwarp();
+    __syncthreads();
   }
-#pragma unroll
-  for (int h = 0; h < GH; ++h) {
-#pragma unroll
-    for (int o = 4; o < 32; o <<= 1) l[h] += __shfl_xor_sync(0xffffffffu, l[h], o);
-    if (lane == 0) sm[w][h] = m[h], sl[w][h] = l[h];
-#pragma unroll
-    for (int i = 0; i < VPL; ++i) so[w][h][lane * VPL + i] = acc[h][i];
+};
+
+// ------------------------------------------------------------------ split
+
+__device__ __forceinline__ int length_of(const PagedAttnArgs& a, int b, int* err) {
+  const int cap = a.width * a.pool.rows, len = a.len[b];
+  if (len >= 0 && len <= cap) return len;
+  report_error(err, DEV_BAD_LENGTH);
+  return len < 0 ? 0 : cap;
+}
+__device__ __forceinline__ int first_of(const PagedAttnArgs& a, int len) {
+  return a.window > 0 ? max(0, len - a.window) : 0;
+}
+// Steps of each unit of sequence b; one without positions takes one, that writes its zeros.
+template <int STEP>
+__device__ __forceinline__ int steps_of(const PagedAttnArgs& a, int b) {
+  const int len = length_of(a, b, nullptr);
+  return max(1, (len - first_of(a, len) + STEP - 1) / STEP);
+}
+
+struct Share {
+  int b, unit, step;    // where the CTA starts
+  long long steps, all;  // how many steps it takes, and how many there are
+  int ctas;              // that take any
+};
+
+// CTA c's share of all steps.
+template <int STEP>
+__device__ __forceinline__ void share_of(const PagedAttnArgs& a, const Plan& plan, int c, Share* out) {
+  __shared__ long long warp_sum[kWarps];
+  const int tid = threadIdx.x, per = (a.seqs + kThreads - 1) / kThreads;
+  const int lo = min(a.seqs, tid * per), hi = min(a.seqs, lo + per);
+  const int units = a.pool.heads * plan.chunks;
+  long long mine = 0;
+  for (int b = lo; b < hi; ++b) mine += steps_of<STEP>(a, b);
+  mine *= units;
+  long long upto = mine;  // inclusive prefix over the threads
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long x = __shfl_up_sync(0xffffffffu, upto, o);
+    if ((tid & 31) >= o) upto += x;
+  }
+  if ((tid & 31) == 31) warp_sum[tid >> 5] = upto;
+  __syncthreads();
+  long long all = 0;
+  for (int w = 0; w < kWarps; ++w) {
+    if (w < tid >> 5) upto += warp_sum[w];
+    all += warp_sum[w];
+  }
+  const long long worth = (all + plan.min_steps - 1) / plan.min_steps;
+  const int ctas = (int)(worth < plan.ctas ? worth : plan.ctas);
+  const long long x0 = c * all / ctas, x1 = (c + 1) * all / ctas;
+  if (tid == 0) out->steps = c < ctas ? x1 - x0 : 0, out->all = all, out->ctas = ctas;
+  if (c < ctas && x0 >= upto - mine && x0 < upto) {
+    long long x = x0 - (upto - mine);
+    for (int b = lo; b < hi; ++b) {
+      const int n = steps_of<STEP>(a, b);
+      if (x < (long long)n * units) {
+        out->b = b, out->unit = (int)(x / n), out->step = (int)(x % n);
+        break;
+      }
+      x -= (long long)n * units;
+    }
   }
   __syncthreads();
-  for (int i = tid; i < nh * D; i += kWarps * 32) {
+}
+
+// The warps' results joined, as a unit's output (slot < 0) or as a part.
+template <class E, int D>
+__device__ __forceinline__ void put(const PagedAttnArgs& a, const Plan& plan, const Unit& u, const Joint<D>& joint,
+                                    long long slot) {
+  for (int i = threadIdx.x; i < u.nh * D; i += kThreads) {
     const int h = i / D, e = i % D;
-    float mx = sm[0][h], sum = 0.f, o = 0.f;
+    float mx = joint.m[0][h], sum = 0.f, o = 0.f;
 #pragma unroll
-    for (int k = 1; k < kWarps; ++k) mx = fmaxf(mx, sm[k][h]);
+    for (int k = 1; k < kWarps; ++k) mx = fmaxf(mx, joint.m[k][h]);
     const float base = mx == -INFINITY ? 0.f : mx;
 #pragma unroll
     for (int k = 0; k < kWarps; ++k) {
-      const float f = exp2f(sm[k][h] - base);
-      sum += f * sl[k][h];
-      o += f * so[k][h][e];
+      const float f = exp2f(joint.m[k][h] - base);
+      sum += f * joint.l[k][h];
+      o += f * joint.o[k][h][e];
     }
-    st_f((T*)a.o + b * a.o_seq + (h0 + h) * a.o_head + e, sum == 0.f ? 0.f : o / sum);
-    if (a.lse && e == 0)
-      a.lse[(long long)b * a.q_heads + h0 + h] = sum == 0.f ? -INFINITY : (base + log2f(sum)) * 0.6931471805599453f;
+    if (slot < 0) {
+      st_f((typename E::T*)a.o + u.b * a.o_seq + (u.h0 + h) * a.o_head + e, sum == 0.f ? 0.f : o / sum);
+      if (a.lse && e == 0)
+        a.lse[(long long)u.b * a.q_heads + u.h0 + h] = sum == 0.f ? -INFINITY : (base + log2f(sum)) * kLn2;
+    } else {
+      plan.acc[(slot * kHeadsMax + h) * D + e] = o;
+      if (e == 0) plan.ml[slot * kHeadsMax + h] = make_float2(mx, sum);
+    }
   }
 }
 
-template <typename T, typename C, int D>
-void attn_d(const PagedAttnArgs& a, int* err, cudaStream_t s) {
-  const int group = a.q_heads / a.pool.heads;
-  const int gh = group <= 1 ? 1 : group <= 2 ? 2 : group <= 4 ? 4 : 8, chunks = (group + gh - 1) / gh;
-  const unsigned grid = (unsigned)((long long)a.seqs * a.pool.heads * chunks);
-  if (gh == 1) launch_kernel(k_attn_paged<T, C, D, 1>, grid, kWarps * 32, 0, s, a, chunks, err);
-  if (gh == 2) launch_kernel(k_attn_paged<T, C, D, 2>, grid, kWarps * 32, 0, s, a, chunks, err);
-  if (gh == 4) launch_kernel(k_attn_paged<T, C, D, 4>, grid, kWarps * 32, 0, s, a, chunks, err);
-  if (gh == 8) launch_kernel(k_attn_paged<T, C, D, 8>, grid, kWarps * 32, 0, s, a, chunks, err);
+template <class E, int D>
+__global__ void __launch_bounds__(kThreads, E::kCtas) k_attn_paged(const PagedAttnArgs a, const Plan plan, int* err) {
+  extern __shared__ __align__(128) unsigned char smem[];
+  __shared__ Share share;
+  pdl_wait();
+  pdl_trigger();
+  const int units = a.pool.heads * plan.chunks, group = a.q_heads / a.pool.heads;
+  int b, unit, step;
+  long long left;
+  if (plan.ctas == 0) {
+    b = blockIdx.x / units, unit = blockIdx.x % units, step = 0, left = 1ll << 40;
+  } else {
+    share_of<E::kStep>(a, plan, blockIdx.x, &share);
+    if (threadIdx.x == 0) plan.meta[blockIdx.x] = make_int4(0, 0, -1, 0);
+    b = share.b, unit = share.unit, step = share.step, left = share.steps;
+  }
+  while (left > 0) {
+    Unit u;
+    u.b = b, u.kh = unit / plan.chunks;
+    const int skip = unit % plan.chunks * plan.gh;
+    u.h0 = u.kh * group + skip, u.nh = min(plan.gh, group - skip);
+    u.len = length_of(a, b, err), u.first = first_of(a, u.len);
+    u.table = a.table + b * a.table_stride;
+    const int steps = max(1, (u.len - u.first + E::kStep - 1) / E::kStep);
+    const int n = (int)min((long long)(steps - step), left);
+    const int p0 = u.first + step * E::kStep;
+    const int p1 = n < steps - step ? p0 + n * E::kStep : u.len;
+    E::run(a, u, p0, p1, smem, err);
+    long long slot = -1;
+    if (n < steps) {
+      slot = blockIdx.x * 2ll + (step == 0);
+      if (step == 0 && threadIdx.x == 0) {
+        // the unit's last step is the (x + 1)-th of all, x + 1 - its share's start = steps
+        const long long start = (long long)blockIdx.x * share.all / share.ctas + (share.steps - left);
+        plan.meta[blockIdx.x] = make_int4(b, unit, (int)(((start + steps) * share.ctas - 1) / share.all), 0);
+      }
+    }
+    put<E, D>(a, plan, u, *reinterpret_cast<const Joint<D>*>(smem), slot);
+    if (plan.ctas == 0) break;
+    left -= n, step = 0;
+    if (++unit == units) unit = 0, ++b;
+    __syncthreads();
+  }
 }
 
-template <typename T, typename C>
-void attn_c(const PagedAttnArgs& a, int* err, cudaStream_t s) {
+// Joins the parts of the unit that starts in CTA blockIdx.x, head blockIdx.y.
+constexpr int kJoinThreads = 256;
+template <typename T, int D>
+__global__ void __launch_bounds__(kJoinThreads) k_attn_join(const PagedAttnArgs a, const Plan plan) {
+  constexpr int L = D / 4, G = kJoinThreads / L;  // lanes of a part, parts at a time
+  __shared__ float red[kJoinThreads / 32];
+  __shared__ float4 so[G][L];
+  __shared__ float sl[G];
+  pdl_wait();
+  pdl_trigger();
+  const int c = blockIdx.x, h = blockIdx.y, tid = threadIdx.x, group = a.q_heads / a.pool.heads;
+  const int4 meta = plan.meta[c];
+  const int skip = meta.y % plan.chunks * plan.gh;
+  if (meta.z < 0 || h >= min(plan.gh, group - skip)) return;
+  const int parts = meta.z - c + 1;
+  // the first part is slot 1 of CTA c, the others slot 0 of the CTAs after it
+  auto slot = [&](int i) { return ((long long)(c + i) * 2 + (i == 0)) * kHeadsMax + h; };
+  float mx = -INFINITY;
+  for (int i = tid; i < parts; i += kJoinThreads) mx = fmaxf(mx, plan.ml[slot(i)].x);
+  mx = warp_max(mx);
+  if ((tid & 31) == 0) red[tid >> 5] = mx;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kJoinThreads / 32; ++w) mx = fmaxf(mx, red[w]);
+  const float base = mx == -INFINITY ? 0.f : mx;
+  const int e = tid % L, g = tid / L;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  float l = 0.f;
+#pragma unroll 4
+  for (int i = g; i < parts; i += G) {
+    const float2 ml = plan.ml[slot(i)];
+    const float4 x = reinterpret_cast<const float4*>(plan.acc + slot(i) * D)[e];
+    const float f = exp2f(ml.x - base);
+    l += f * ml.y;
+    o.x += f * x.x, o.y += f * x.y, o.z += f * x.z, o.w += f * x.w;
+  }
+  so[g][e] = o;
+  if (e == 0) sl[g] = l;
+  __syncthreads();
+  if (tid < D) {
+    float sum = 0.f, x = 0.f;
+#pragma unroll
+    for (int k = 0; k < G; ++k) sum += sl[k], x += reinterpret_cast<const float*>(so[k])[tid];
+    const int head = meta.y / plan.chunks * group + skip + h;
+    st_f((T*)a.o + meta.x * a.o_seq + head * a.o_head + tid, sum == 0.f ? 0.f : x / sum);
+    if (a.lse && tid == 0) a.lse[(long long)meta.x * a.q_heads + head] = sum == 0.f ? -INFINITY : (base + log2f(sum)) * kLn2;
+  }
+}
+
+// ------------------------------------------------------------------ host
+
+// CTAs of k_attn_paged<E, D> that the current device holds at once.
+template <class E, int D>
+int resident_ctas() {
+  static PerDevice cache;
+  return cache.get([] {
+    int per_sm = 0;
+    cudaFuncSetAttribute(k_attn_paged<E, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, E::kSmem);
+    cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, k_attn_paged<E, D>, kThreads, E::kSmem);
+    return device_sm_count() * (per_sm > 0 ? per_sm : 1);
+  });
+}
+
+constexpr int kMinSteps = 2;
+
+template <class E, int D>
+cudaError_t attn_e(const PagedAttnArgs& a, int gh, int* err, cudaStream_t s) {
+  const int group = a.q_heads / a.pool.heads;
+  Plan plan = {};
+  plan.gh = gh, plan.chunks = (group + gh - 1) / gh;
+  plan.min_steps = kMinSteps;
+  const long long units = (long long)a.seqs * a.pool.heads * plan.chunks;
+  long long most = (long long)a.width * a.pool.rows;  // positions of a unit
+  if (a.window > 0 && a.window < most) most = a.window;
+  const long long steps = (most + E::kStep - 1) / E::kStep;
+  const int slots = resident_ctas<E, D>();
+  float* scratch = nullptr;
+  if (steps > kMinSteps && units < 8ll * slots) {
+    const long long worth = units * steps;
+    plan.ctas = (int)(worth < slots ? worth : slots);
+    const size_t parts = (size_t)plan.ctas * 2 * kHeadsMax;
+    const size_t bytes = parts * (D * sizeof(float) + sizeof(float2)) + plan.ctas * sizeof(int4);
+    const cudaError_t e = scratch_malloc((void**)&scratch, bytes, s);
+    if (e != cudaSuccess) return e;
+    plan.acc = scratch;
+    plan.ml = (float2*)(scratch + parts * D);
+    plan.meta = (int4*)(plan.ml + parts);
+  }
+  launch_kernel(k_attn_paged<E, D>, plan.ctas ? (unsigned)plan.ctas : (unsigned)units, kThreads, E::kSmem, s, a, plan, err);
+  if (!scratch) return cudaGetLastError();
+  launch_kernel(k_attn_join<typename E::T, D>, dim3(plan.ctas, group < gh ? group : gh), kJoinThreads, 0, s, a, plan);
+  const cudaError_t e = cudaGetLastError(), f = cudaFreeAsync(scratch, s);
+  return e != cudaSuccess ? e : f;
+}
+
+template <typename C, int D>
+cudaError_t attn_d(int dt, const PagedAttnArgs& a, int* err, cudaStream_t s) {
+  const int group = a.q_heads / a.pool.heads;
+  if constexpr (!std::is_same<C, float>::value)
+    if (dt == DT_BF16) return attn_e<TensorCores<C, D>, D>(a, kHeadsMax, err, s);
+  if constexpr (!std::is_same<C, bf16>::value) {
+    if (group <= 1) return attn_e<CudaCores<C, D, 1>, D>(a, 1, err, s);
+    if (group <= 2) return attn_e<CudaCores<C, D, 2>, D>(a, 2, err, s);
+    if (group <= 4) return attn_e<CudaCores<C, D, 4>, D>(a, 4, err, s);
+    return attn_e<CudaCores<C, D, 8>, D>(a, 8, err, s);
+  }
+  return cudaErrorInvalidValue;
+}
+
+template <typename C>
+cudaError_t attn_c(int dt, const PagedAttnArgs& a, int* err, cudaStream_t s) {
   switch (a.pool.dh) {
-    case 32: return attn_d<T, C, 32>(a, err, s);
-    case 64: return attn_d<T, C, 64>(a, err, s);
-    case 128: return attn_d<T, C, 128>(a, err, s);
-    case 256: return attn_d<T, C, 256>(a, err, s);
+    case 32: return attn_d<C, 32>(dt, a, err, s);
+    case 64: return attn_d<C, 64>(dt, a, err, s);
+    case 128: return attn_d<C, 128>(dt, a, err, s);
+    default: return attn_d<C, 256>(dt, a, err, s);
   }
 }
 
 }  // namespace
 
-void launch_attn_paged(int dt, const PagedAttnArgs& a, int* err, cudaStream_t s) {
-  if (dt == DT_F32) {
-    if (a.pool.kind == 0) attn_c<float, float>(a, err, s);
-    if (a.pool.kind == 2) attn_c<float, e4m3>(a, err, s);
-    if (a.pool.kind == 3) attn_c<float, int8_t>(a, err, s);
-  } else {
-    if (a.pool.kind == 1) attn_c<bf16, bf16>(a, err, s);
-    if (a.pool.kind == 2) attn_c<bf16, e4m3>(a, err, s);
-    if (a.pool.kind == 3) attn_c<bf16, int8_t>(a, err, s);
+cudaError_t launch_attn_paged(int dt, const PagedAttnArgs& a, int* err, cudaStream_t s) {
+  switch (a.pool.kind) {
+    case 0: return attn_c<float>(dt, a, err, s);
+    case 1: return attn_c<bf16>(dt, a, err, s);
+    case 2: return attn_c<e4m3>(dt, a, err, s);
+    default: return attn_c<int8_t>(dt, a, err, s);
   }
 }
 

@@ -402,7 +402,11 @@ void launch_kv_write(int dt, const KvPoolArgs& p, const KvPlaceArgs& pl, const H
                      const RopeArgs* r, const HeadsArgs& q, int* err, cudaStream_t s);
 void launch_kv_read(int dt, const KvPoolArgs& p, const KvPlaceArgs& pl, const HeadsArgs& k, const HeadsArgs& v,
                     int* err, cudaStream_t s);
-void launch_attn_paged(int dt, const PagedAttnArgs& a, int* err, cudaStream_t s);
+// Takes the scratch of its split from scratch_malloc and returns it on the stream.
+cudaError_t launch_attn_paged(int dt, const PagedAttnArgs& a, int* err, cudaStream_t s);
+
+// Stream-ordered memory from the library's pool of the current device (runtime.cu); cudaFreeAsync returns it.
+cudaError_t scratch_malloc(void** p, size_t bytes, cudaStream_t s);
 
 // ---- error message of the calling thread (read by photon_last_error) ----
 void set_error_message(const char* msg);

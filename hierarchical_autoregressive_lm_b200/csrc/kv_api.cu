@@ -19,12 +19,12 @@ static int refuse(const char* fmt, ...) {
   return PHOTON_ERR_ARG;
 }
 
-static int launched() {
-  const cudaError_t e = cudaGetLastError();
+static int result(cudaError_t e) {
   if (e == cudaSuccess) return PHOTON_OK;
   set_error_message(cudaGetErrorString(e));
-  return PHOTON_ERR_CUDA;
+  return e == cudaErrorMemoryAllocation ? PHOTON_ERR_OOM : PHOTON_ERR_CUDA;
 }
+static int launched() { return result(cudaGetLastError()); }
 
 static bool aligned_to(const void* p, size_t n) { return (uintptr_t)p % n == 0; }
 
@@ -76,7 +76,7 @@ static int check_pool(const photon_kv_pages* p, int dtype, KvPoolArgs* out) {
 static int check_table(const photon_kv_pages* p, const int32_t* table, int32_t seqs, int32_t width) {
   if (seqs <= 0 || width <= 0) return refuse("table: empty shape [%d, %d]", seqs, width);
   if (!table || !aligned_to(table, 4)) return refuse("table: NULL or misaligned");
-  if ((int64_t)width * p->page_rows > INT32_MAX) return refuse("table: width * page_rows must be below 2^31");
+  if ((int64_t)width * p->page_rows > (1 << 30)) return refuse("table: more than 2^30 positions a sequence");
   return PHOTON_OK;
 }
 
@@ -233,8 +233,7 @@ int photon_attn_decode_paged(const photon_kv_pages* pages, int32_t dtype, const 
   a.q = d_q, a.q_seq = q_seq, a.q_head = q_head, a.q_heads = q_heads;
   a.window = window, a.scale = scale;
   a.o = d_o, a.o_seq = o_seq, a.o_head = o_head, a.lse = d_lse;
-  launch_attn_paged(dtype, a, d_err, (cudaStream_t)stream);
-  return launched();
+  return result(launch_attn_paged(dtype, a, d_err, (cudaStream_t)stream));
 }
 
 }  // extern "C"

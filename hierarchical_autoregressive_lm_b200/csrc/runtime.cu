@@ -288,6 +288,7 @@ static cudaError_t pool_malloc(void** p, size_t bytes, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   return cudaMallocFromPoolAsync(p, bytes, pool, s);
 }
+cudaError_t photon::scratch_malloc(void** p, size_t bytes, cudaStream_t s) { return pool_malloc(p, bytes, s); }
 
 // Draws (or fills) every tensor of one group into its buffer.
 static void generate_group(photon_model* m, int g, cudaStream_t s) {

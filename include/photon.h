@@ -708,7 +708,7 @@ typedef struct photon_kv_pages {
 /* Where positions live: d_table [seqs][width] (device int32, rows
  * table_stride apart) names the page of positions r * page_rows .. of each
  * sequence.  Entries past a sequence's positions are never read.  width *
- * page_rows and tokens * heads are below 2^31.  A sequence index, position or
+ * page_rows is at most 2^30, tokens * heads below 2^31.  A sequence index, position or
  * page outside its range is left out (nothing is read or written for it) and
  * reported in the error word d_err (device int32, nullable; zeroed by the
  * caller, set to a nonzero code by the kernels).
