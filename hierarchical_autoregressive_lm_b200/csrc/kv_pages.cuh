@@ -111,13 +111,22 @@ __device__ __forceinline__ void store8(e4m3* p, const float (&v)[8]) {
     w[i] = __nv_cvt_float2_to_fp8x2(make_float2(v[2 * i], v[2 * i + 1]), __NV_SATFINITE, __NV_E4M3);
   *reinterpret_cast<uint2*>(p) = make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
 }
+// v rounded to a whole number (|v| below 2^22) in the low bits of the sum: the
+// conversion instruction runs at a quarter of an addition's rate.
+__device__ __forceinline__ uint32_t whole(float v) { return __float_as_uint(__fadd_rn(v, 12582912.f)); }
 template <bool VEC>
 __device__ __forceinline__ void store8(int8_t* p, const float (&v)[8]) {
-  uint32_t w[2] = {0, 0};
+  uint32_t w[2];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) w[i / 4] |= (uint32_t)(uint8_t)(int8_t)__float2int_rn(v[i]) << (8 * (i % 4));
+  for (int i = 0; i < 2; ++i)
+    w[i] = __byte_perm(__byte_perm(whole(v[4 * i]), whole(v[4 * i + 1]), 0x0040),
+                       __byte_perm(whole(v[4 * i + 2]), whole(v[4 * i + 3]), 0x0040), 0x5410);
   *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
 }
+__device__ __forceinline__ void store1(float* p, float v) { *p = v; }
+__device__ __forceinline__ void store1(bf16* p, float v) { *p = __float2bfloat16_rn(v); }
+__device__ __forceinline__ void store1(e4m3* p, float v) { p->x = __nv_cvt_float_to_fp8(v, __NV_SATFINITE, __NV_E4M3); }
+__device__ __forceinline__ void store1(int8_t* p, float v) { *p = (int8_t)whole(v); }
 
 // Page and row of position `pos` of a sequence; false where there is none
 // (reported, so that nothing is read or written for it).
