@@ -30,56 +30,62 @@ __device__ __forceinline__ void turn(unsigned long long freq, int pos, float sca
   *c *= scale;
 }
 
-// One launch's split: a block takes `tokens` tokens of `items` threads' work
-// each (rows * chunks), or one of `parts` spans of one token's items.
+// The split of one tensor's rows [tokens][heads]: a block takes `tokens`
+// tokens, or one of `parts` spans of one token's rows.  `chunks` threads
+// share a row, always the same part of it, and the block's kThreads / chunks
+// groups take rows in turn.
 struct Split {
-  int tokens, items, chunks, parts, span, blocks;
-  FastDiv by_items, by_chunks, by_half, by_parts;
+  int heads, chunks, tokens, parts, span, blocks;
+  FastDiv by_heads, by_chunks, by_half, by_parts;
 };
 
-Split split_rows(int n, int rows, int chunks, int rot) {
-  // 1024 items a block (four a thread) keep enough bytes in flight; calls too
-  // small to give every SM two such blocks take 256
+// work: threads' items in the whole launch.
+Split split_rows(int n, int heads, int chunks, int rot, long long work) {
+  // four rows a group keep enough bytes in flight and share the block's
+  // angles; calls too small to give every SM two such blocks take one
   Split s = {};
-  s.items = rows * chunks, s.chunks = chunks;
-  s.span = (long long)n * s.items >= 2048ll * device_sm_count() ? 4 * kThreads : kThreads;
-  s.tokens = s.span / s.items < 1 ? 1 : s.span / s.items;
+  const int groups = kThreads / chunks;
+  s.heads = heads, s.chunks = chunks;
+  s.span = work >= 2ll * 4 * kThreads * device_sm_count() ? 4 * groups : groups;
+  s.tokens = s.span / heads < 1 ? 1 : s.span / heads;
   if (s.tokens > kTokensMax) s.tokens = kTokensMax;
   if (rot && s.tokens > kAnglesMax / rot) s.tokens = kAnglesMax / rot;
   if (s.tokens > n) s.tokens = n;
-  s.parts = s.tokens > 1 ? 1 : (s.items + s.span - 1) / s.span;
-  if (s.parts == 1) s.span = s.tokens * s.items;
+  s.parts = s.tokens > 1 ? 1 : (heads + s.span - 1) / s.span;
+  if (s.parts == 1) s.span = s.tokens * heads;
   s.blocks = (n + s.tokens - 1) / s.tokens * s.parts;
-  s.by_items = fast_div((uint32_t)s.items);
+  s.by_heads = fast_div((uint32_t)heads);
   s.by_chunks = fast_div((uint32_t)chunks);
   s.by_half = fast_div(rot ? (uint32_t)rot / 2 : 1u);
   s.by_parts = fast_div((uint32_t)s.parts);
   return s;
 }
 
-// What a block does of it: tokens t0 .. t0 + n - 1, items lo .. hi - 1 of them.
+// What a block does of it: tokens t0 .. t0 + n - 1, rows first .. end - 1 of
+// theirs for this thread, every `step`-th, part c of each.
 struct Range {
-  int t0, n, lo, hi;
+  int t0, n, first, end, step, c;
 };
 __device__ __forceinline__ Range range_of(const Split& s, int block, int tokens) {
   Range r;
-  const int group = (int)div_fast((uint32_t)block, s.by_parts);
+  const int group = (int)div_fast((uint32_t)block, s.by_parts), lo = (block - group * s.parts) * s.span;
   r.t0 = group * s.tokens;
   r.n = min(s.tokens, tokens - r.t0);
-  r.lo = (block - group * s.parts) * s.span;
-  r.hi = min(r.n * s.items, r.lo + s.span);
+  r.step = (int)div_fast(kThreads, s.by_chunks);
+  const int mine = (int)div_fast(threadIdx.x, s.by_chunks);
+  r.c = threadIdx.x - mine * s.chunks;
+  r.first = lo + mine;
+  r.end = mine < r.step ? min(r.n * s.heads, lo + s.span) : 0;
   return r;
 }
-struct Item {
-  int token, row, c;  // token within the block
+struct Row {
+  int token, head;  // token within the block
 };
-__device__ __forceinline__ Item item_of(const Split& s, int i) {
-  Item it;
-  it.token = (int)div_fast((uint32_t)i, s.by_items);
-  const uint32_t rest = i - it.token * s.items;
-  it.row = (int)div_fast(rest, s.by_chunks);
-  it.c = (int)rest - it.row * s.chunks;
-  return it;
+__device__ __forceinline__ Row row_of(const Split& s, int i) {
+  Row r;
+  r.token = (int)div_fast((uint32_t)i, s.by_heads);
+  r.head = i - r.token * s.heads;
+  return r;
 }
 
 // Cosines [rot / 2], then sines, of each of the block's tokens.
@@ -169,75 +175,70 @@ template <typename T> struct Raw8 {
   }
 };
 
-// Items a thread has in flight: 64 bytes of rows.
+// Rows a thread has in flight: 64 bytes of its parts.
 template <typename T> constexpr int kAhead = 4 / sizeof(T);
 
+// Blocks below sa.blocks take rows of a, the others of b.
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(kThreads) k_rope(const RopeArgs r, const int* __restrict__ pos, int n, int dh,
-                                                   const HeadsArgs a, const HeadsArgs b, bool back, const Split s) {
+                                                   const HeadsArgs a, const HeadsArgs b, bool back, const Split sa,
+                                                   const Split sb) {
   __shared__ __align__(16) float angles[kAnglesMax];
   pdl_wait();
   pdl_trigger();
-  const Range range = range_of(s, blockIdx.x, n);
-  auto row_in = [&](const Item& it) {
-    const HeadsArgs& t = it.row < a.heads ? a : b;
-    const int h = it.row < a.heads ? it.row : it.row - a.heads;
-    return (const T*)t.in + (range.t0 + it.token) * t.in_tok + h * t.in_head;
-  };
-  auto row_out = [&](const Item& it) {
-    const HeadsArgs& t = it.row < a.heads ? a : b;
-    const int h = it.row < a.heads ? it.row : it.row - a.heads;
-    return (T*)t.out + (range.t0 + it.token) * t.out_tok + h * t.out_head;
-  };
+  const bool second = (int)blockIdx.x >= sa.blocks;
+  const Split s = second ? sb : sa;
+  const HeadsArgs t = second ? b : a;
+  const Range range = range_of(s, second ? blockIdx.x - sa.blocks : blockIdx.x, n);
+  const T* const in = (const T*)t.in + range.t0 * t.in_tok;
+  T* const out = (T*)t.out + range.t0 * t.out_tok;
   if constexpr (VEC) {
     constexpr int U = kAhead<T>;
+    int e0, e1;
+    vectors_of(e0, e1, range.c, r.rot, dh);
     Raw8<T> x[U], y[U];
     auto fetch = [&](int i0) {
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const int i = i0 + u * kThreads;
-        if (i >= range.hi) continue;
-        const Item it = item_of(s, i);
-        int e0, e1;
-        vectors_of(e0, e1, it.c, r.rot, dh);
-        const T* p = row_in(it);
+        const int i = i0 + u * range.step;
+        if (i >= range.end) continue;
+        const Row row = row_of(s, i);
+        const T* p = in + row.token * t.in_tok + row.head * t.in_head;
         x[u].load(p + e0), y[u].load(p + e1);
       }
     };
-    int i0 = range.lo + threadIdx.x;
+    int i0 = range.first;
     fetch(i0);
     fill_angles(angles, r, s, range, pos, back);
     __syncthreads();
-    while (i0 < range.hi) {
+    while (i0 < range.end) {
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const int i = i0 + u * kThreads;
-        if (i >= range.hi) continue;
-        const Item it = item_of(s, i);
-        int e0, e1;
-        vectors_of(e0, e1, it.c, r.rot, dh);
+        const int i = i0 + u * range.step;
+        if (i >= range.end) continue;
+        const Row row = row_of(s, i);
         float v[8], w[8];
         x[u].get(v), y[u].get(w);
-        if (it.c < r.rot / 16) rotate16(v, w, it.c, angles + it.token * r.rot, r);
-        T* p = row_out(it);
+        if (range.c < r.rot / 16) rotate16(v, w, range.c, angles + row.token * r.rot, r);
+        T* p = out + row.token * t.out_tok + row.head * t.out_head;
         store8<true>(p + e0, v);
         store8<true>(p + e1, w);
       }
-      i0 += U * kThreads;
+      i0 += U * range.step;
       fetch(i0);
     }
   } else {
     fill_angles(angles, r, s, range, pos, back);
     __syncthreads();
-    for (int i = range.lo + threadIdx.x; i < range.hi; i += kThreads) {
-      const Item it = item_of(s, i);
-      int e0, e1;
-      pair_of(e0, e1, it.c, r);
-      const T* p = row_in(it);
+    int e0, e1;
+    pair_of(e0, e1, range.c, r);
+    for (int i = range.first; i < range.end; i += range.step) {
+      const Row row = row_of(s, i);
+      const T* p = in + row.token * t.in_tok + row.head * t.in_head;
       float x = ld_f(p + e0), y = ld_f(p + e1);
-      const float* f = angles + it.token * r.rot + it.c;
-      if (it.c < r.rot / 2) rotate(x, y, f[0], f[r.rot / 2]);
-      T* o = row_out(it);
+      const float* f = angles + row.token * r.rot + range.c;
+      if (range.c < r.rot / 2) rotate(x, y, f[0], f[r.rot / 2]);
+      T* o = out + row.token * t.out_tok + row.head * t.out_head;
       st_f(o + e0, x), st_f(o + e1, y);
     }
   }
@@ -265,156 +266,187 @@ __device__ __forceinline__ void fill_places(Places& out, const KvPoolArgs& p, co
 }
 
 // x and y, a row's share of this thread, as codes: the row's threads (a group
-// of `lanes` of the warp) agree on its scale.  |x| is compared as bits: the
-// order of unsigned numbers is that of magnitudes, with infinities and NaN
-// above every number.
+// of `lanes` of the warp, at least two) agree on its scale.  `m` is the
+// largest of this thread's magnitudes as bits: the order of unsigned numbers
+// is that of magnitudes, with infinities and NaN above every number.  The
+// group's first thread divides for the scale, the others for the codes, in
+// one instruction sequence.
 template <typename C>
-__device__ __forceinline__ void quantise16(float (&x)[8], float (&y)[8], float* scale, int lanes, bool first) {
+__device__ __forceinline__ void quantise16(float (&x)[8], float (&y)[8], uint32_t m, float* scale, int lanes, bool first) {
+  const int lead = threadIdx.x & 31 & ~(lanes - 1);
+  const unsigned mask = ((1u << lanes) - 1) << lead;
+  for (int o = lanes / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(mask, m, o));
+  const float amax = fmaxf(__uint_as_float(m), 1e-30f), top = KvKind<C>::top;
+  const float q = (first ? amax : top) / (first ? top : amax);
+  const float inv = __shfl_sync(mask, q, lead + 1);
+  const bool fine = m < 0x7f800000u;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) x[i] *= inv, y[i] *= inv;
+  if (!fine) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = y[i] = 0.f;
+  }
+  if (first) *scale = fine ? q : __uint_as_float(0x7fffffffu);
+}
+__device__ __forceinline__ uint32_t largest(const float (&x)[8], const float (&y)[8]) {
   uint32_t m = 0;
 #pragma unroll
   for (int i = 0; i < 8; ++i) m = max(m, max(__float_as_uint(x[i]) & 0x7fffffffu, __float_as_uint(y[i]) & 0x7fffffffu));
-  const unsigned mask = ((1u << lanes) - 1) << (threadIdx.x & 31 & ~(lanes - 1));
-  for (int o = lanes / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(mask, m, o));
-  const float amax = fmaxf(__uint_as_float(m), 1e-30f);
-  const bool fine = m < 0x7f800000u;
-  const float inv = fine ? KvKind<C>::top / amax : 0.f;
+  return m;
+}
+// The same of bf16 pairs as they were loaded, two at a time.
+__device__ __forceinline__ uint32_t largest(const Raw8<bf16>& x, const Raw8<bf16>& y) {
+  uint32_t m = 0;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    x[i] = fine ? x[i] * inv : 0.f;
-    y[i] = fine ? y[i] * inv : 0.f;
-  }
-  if (first) *scale = fine ? amax / KvKind<C>::top : __uint_as_float(0x7fffffffu);
+  for (int i = 0; i < 4; ++i) m = __vmaxu2(m, __vmaxu2(x.w[i] & 0x7fff7fffu, y.w[i] & 0x7fff7fffu));
+  return max(m << 16, m & 0xffff0000u);
 }
 
-// Rows of a token: key heads, value heads, query heads (rotated into q.out).
+// Blocks below sk.blocks take key rows, as many after them value rows, the
+// others query rows, which are rotated into q.out.
 template <typename T, typename C, bool VEC>
 __global__ void __launch_bounds__(kThreads) k_kv_write(const KvPoolArgs p, const KvPlaceArgs pl, const HeadsArgs k,
                                                        const HeadsArgs v, const RopeArgs r, const HeadsArgs q,
-                                                       const Split s, int* err) {
+                                                       const Split sk, const Split sq, int* err) {
   __shared__ __align__(16) float angles[kAnglesMax];
   __shared__ Places places;
   pdl_wait();
   pdl_trigger();
-  const Range range = range_of(s, blockIdx.x, pl.tokens);
-  auto row_in = [&](const Item& it) {
-    const HeadsArgs& t = it.row < p.heads ? k : it.row < 2 * p.heads ? v : q;
-    const int h = it.row < p.heads ? it.row : it.row < 2 * p.heads ? it.row - p.heads : it.row - 2 * p.heads;
-    return (const T*)t.in + (range.t0 + it.token) * t.in_tok + h * t.in_head;
-  };
-  auto turns = [&](const Item& it) { return r.rot > 0 && (it.row < p.heads || it.row >= 2 * p.heads); };
+  const bool query = (int)blockIdx.x >= 2 * sk.blocks, value = !query && (int)blockIdx.x >= sk.blocks;
+  const int block = blockIdx.x - (query ? 2 : value ? 1 : 0) * sk.blocks;
+  const Split s = query ? sq : sk;
+  const HeadsArgs t = query ? q : value ? v : k;
+  const Range range = range_of(s, block, pl.tokens);
+  const T* const in = (const T*)t.in + range.t0 * t.in_tok;
+  const bool turns = r.rot > 0 && !value;
   constexpr int U = VEC ? kAhead<T> : 1;
   Raw8<T> rx[U], ry[U];
+  int e0 = 0, e1 = 0;
+  if constexpr (VEC) vectors_of(e0, e1, range.c, r.rot, p.dh);
   auto fetch = [&](int i0) {
     if constexpr (VEC) {
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const int i = i0 + u * kThreads;
-        if (i >= range.hi) continue;
-        const Item it = item_of(s, i);
-        int e0, e1;
-        vectors_of(e0, e1, it.c, r.rot, p.dh);
-        const T* in = row_in(it);
-        rx[u].load(in + e0), ry[u].load(in + e1);
+        const int i = i0 + u * range.step;
+        if (i >= range.end) continue;
+        const Row row = row_of(s, i);
+        const T* from = in + row.token * t.in_tok + row.head * t.in_head;
+        rx[u].load(from + e0), ry[u].load(from + e1);
       }
     }
   };
-  int i0 = range.lo + threadIdx.x;
+  int i0 = range.first;
   fetch(i0);
-  if (r.rot) fill_angles(angles, r, s, range, pl.pos, false);
-  fill_places(places, p, pl, range, err);
+  if (turns) fill_angles(angles, r, s, range, pl.pos, false);
+  if (query) {  // follows its position alone, whether or not its place exists
+    for (int i = threadIdx.x; i < range.n; i += kThreads) places.at[i] = pl.pos[range.t0 + i] < 0 ? -1 : 0;
+  } else {
+    fill_places(places, p, pl, range, err);
+  }
   __syncthreads();
-  while (i0 < range.hi) {
+  C* const pages = (C*)(value ? p.v : p.k);
+  float* const scales = value ? p.v_scale : p.k_scale;
+  while (i0 < range.end) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int i = i0 + u * kThreads;
-      if (i >= range.hi) continue;
-      const Item it = item_of(s, i);
-      const bool query = it.row >= 2 * p.heads;
-      // a query follows its position alone, whether or not its place exists
-      if (query ? pl.pos[range.t0 + it.token] < 0 : places.at[it.token] < 0) continue;
+      const int i = i0 + u * range.step;
+      if (i >= range.end) continue;
+      const Row row = row_of(s, i);
+      const long long at = places.at[row.token];
+      if (at < 0) continue;
       float x[8], y[8];
-      int e0[VEC ? 1 : 8], e1[VEC ? 1 : 8];
-      const float* f = angles + it.token * r.rot;
+      const float* f = angles + row.token * r.rot;
       if constexpr (VEC) {
-        vectors_of(e0[0], e1[0], it.c, r.rot, p.dh);
         rx[u].get(x), ry[u].get(y);
-        if (it.c < r.rot / 16 && turns(it)) rotate16(x, y, it.c, f, r);
+        if (turns && range.c < r.rot / 16) rotate16(x, y, range.c, f, r);
       } else {
-        const T* in = row_in(it);
+        const T* from = in + row.token * t.in_tok + row.head * t.in_head;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          const int pair = 8 * it.c + j;
-          pair_of(e0[j], e1[j], pair, r);
-          x[j] = ld_f(in + e0[j]), y[j] = ld_f(in + e1[j]);
-          if (pair < r.rot / 2 && turns(it)) rotate(x[j], y[j], f[pair], f[r.rot / 2 + pair]);
+          const int pair = 8 * range.c + j;
+          pair_of(e0, e1, pair, r);
+          x[j] = ld_f(from + e0), y[j] = ld_f(from + e1);
+          if (turns && pair < r.rot / 2) rotate(x[j], y[j], f[pair], f[r.rot / 2 + pair]);
         }
       }
       if (query) {
-        T* out = (T*)q.out + (range.t0 + it.token) * q.out_tok + (it.row - 2 * p.heads) * q.out_head;
+        T* out = (T*)q.out + (range.t0 + row.token) * q.out_tok + row.head * q.out_head;
         if constexpr (VEC) {
-          store8<true>(out + e0[0], x), store8<true>(out + e1[0], y);
+          store8<true>(out + e0, x), store8<true>(out + e1, y);
         } else {
 #pragma unroll
-          for (int j = 0; j < 8; ++j) st_f(out + e0[j], x[j]), st_f(out + e1[j], y[j]);
+          for (int j = 0; j < 8; ++j) {
+            pair_of(e0, e1, 8 * range.c + j, r);
+            st_f(out + e0, x[j]), st_f(out + e1, y[j]);
+          }
         }
         continue;
       }
-      const bool value = it.row >= p.heads;
-      const int h = value ? it.row - p.heads : it.row;
-      if constexpr (KvKind<C>::narrow)
-        quantise16<C>(x, y, (value ? p.v_scale : p.k_scale) + places.scale[it.token] + h * p.scale_head, s.chunks, it.c == 0);
-      C* out = (C*)(value ? p.v : p.k) + places.at[it.token] + h * p.head;
+      if constexpr (KvKind<C>::narrow) {
+        uint32_t m;
+        if constexpr (VEC && sizeof(T) == 2)
+          m = turns ? largest(x, y) : largest(rx[u], ry[u]);
+        else
+          m = largest(x, y);
+        quantise16<C>(x, y, m, scales + places.scale[row.token] + row.head * p.scale_head, s.chunks, range.c == 0);
+      }
+      C* out = pages + at + row.head * p.head;
       if constexpr (VEC) {
-        store8<true>(out + e0[0], x), store8<true>(out + e1[0], y);
+        store8<true>(out + e0, x), store8<true>(out + e1, y);
       } else {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) store1(out + e0[j], x[j]), store1(out + e1[j], y[j]);
+        for (int j = 0; j < 8; ++j) {
+          pair_of(e0, e1, 8 * range.c + j, r);
+          store1(out + e0, x[j]), store1(out + e1, y[j]);
+        }
       }
     }
-    i0 += U * kThreads;
+    i0 += U * range.step;
     fetch(i0);
   }
 }
 
+// Blocks below s.blocks take key rows, the others value rows.
 template <typename T, typename C, bool VEC>
 __global__ void __launch_bounds__(kThreads) k_kv_read(const KvPoolArgs p, const KvPlaceArgs pl, const HeadsArgs k,
                                                       const HeadsArgs v, const Split s, int* err) {
   __shared__ Places places;
   pdl_wait();
   pdl_trigger();
-  const Range range = range_of(s, blockIdx.x, pl.tokens);
+  const bool value = (int)blockIdx.x >= s.blocks;
+  const HeadsArgs t = value ? v : k;
+  const Range range = range_of(s, value ? blockIdx.x - s.blocks : blockIdx.x, pl.tokens);
   fill_places(places, p, pl, range, err);
   __syncthreads();
   constexpr int U = kAhead<C>;
-  for (int i0 = range.lo + threadIdx.x; i0 < range.hi; i0 += U * kThreads) {
+  const C* const pages = (const C*)(value ? p.v : p.k) + 8 * range.c;
+  const float* const scales = value ? p.v_scale : p.k_scale;
+  T* const base = (T*)t.out + range.t0 * t.out_tok + 8 * range.c;
+  for (int i0 = range.first; i0 < range.end; i0 += U * range.step) {
     Raw8<C> rx[U], ry[U];
     float scale[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      if (i0 + u * kThreads >= range.hi) continue;
-      const Item it = item_of(s, i0 + u * kThreads);
-      if (places.at[it.token] < 0) continue;
-      const bool value = it.row >= p.heads;
-      const int h = value ? it.row - p.heads : it.row;
-      const C* in = (const C*)(value ? p.v : p.k) + places.at[it.token] + h * p.head + 8 * it.c;
+      if (i0 + u * range.step >= range.end) continue;
+      const Row row = row_of(s, i0 + u * range.step);
+      const long long at = places.at[row.token];
+      if (at < 0) continue;
+      const C* in = pages + at + row.head * p.head;
       rx[u].load(in), ry[u].load(in + p.dh / 2);
-      if constexpr (KvKind<C>::narrow) scale[u] = (value ? p.v_scale : p.k_scale)[places.scale[it.token] + h * p.scale_head];
+      if constexpr (KvKind<C>::narrow) scale[u] = scales[places.scale[row.token] + row.head * p.scale_head];
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      if (i0 + u * kThreads >= range.hi) continue;
-      const Item it = item_of(s, i0 + u * kThreads);
-      if (places.at[it.token] < 0) continue;
-      const bool value = it.row >= p.heads;
-      const int h = value ? it.row - p.heads : it.row;
+      if (i0 + u * range.step >= range.end) continue;
+      const Row row = row_of(s, i0 + u * range.step);
+      if (places.at[row.token] < 0) continue;
       float x[8], y[8];
       rx[u].get(x), ry[u].get(y);
       if constexpr (KvKind<C>::narrow) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) x[j] *= scale[u], y[j] *= scale[u];
       }
-      const HeadsArgs& t = value ? v : k;
-      T* out = (T*)t.out + (range.t0 + it.token) * t.out_tok + h * t.out_head + 8 * it.c;
+      T* out = base + row.token * t.out_tok + row.head * t.out_head;
       store8<VEC>(out, x), store8<VEC>(out + p.dh / 2, y);
     }
   }
@@ -441,27 +473,35 @@ template <typename T>
 void rope_t(const RopeArgs& r, const int* pos, int n, int dh, const HeadsArgs& a, const HeadsArgs& b, bool back,
             cudaStream_t s) {
   const bool vec = rope_vectors<T>(r, dh, a, b);
-  const Split sp = split_rows(n, a.heads + b.heads, vec ? dh / 16 : dh / 2, r.rot);
-  launch_kernel(vec ? k_rope<T, true> : k_rope<T, false>, sp.blocks, kThreads, 0, s, r, pos, n, dh, a, b, back, sp);
+  const int chunks = vec ? dh / 16 : dh / 2;
+  const long long work = (long long)n * (a.heads + b.heads) * chunks;
+  const Split sa = split_rows(n, a.heads, chunks, r.rot, work);
+  const Split sb = b.heads ? split_rows(n, b.heads, chunks, r.rot, work) : Split();
+  launch_kernel(vec ? k_rope<T, true> : k_rope<T, false>, sa.blocks + sb.blocks, kThreads, 0, s, r, pos, n, dh, a, b,
+                back, sa, sb);
 }
 
 template <typename T, typename C>
 void write_t(const KvPoolArgs& p, const KvPlaceArgs& pl, const HeadsArgs& k, const HeadsArgs& v, const RopeArgs* r,
              const HeadsArgs& q, int* err, cudaStream_t s) {
   const RopeArgs rope = r ? *r : RopeArgs();
-  const Split sp = split_rows(pl.tokens, 2 * p.heads + q.heads, p.dh / 16, rope.rot);
+  const int chunks = p.dh / 16;
+  const long long work = (long long)pl.tokens * (2 * p.heads + q.heads) * chunks;
+  const Split sk = split_rows(pl.tokens, p.heads, chunks, rope.rot, work);
+  const Split sq = q.heads ? split_rows(pl.tokens, q.heads, chunks, rope.rot, work) : Split();
   // one choice for the whole launch: rows of k, v and q all in vectors, or none
   const bool vec = aligned<T>(k) && rope_vectors<T>(rope, p.dh, v, q);
-  launch_kernel(vec ? k_kv_write<T, C, true> : k_kv_write<T, C, false>, sp.blocks, kThreads, 0, s, p, pl, k, v, rope, q,
-                sp, err);
+  launch_kernel(vec ? k_kv_write<T, C, true> : k_kv_write<T, C, false>, 2 * sk.blocks + sq.blocks, kThreads, 0, s, p,
+                pl, k, v, rope, q, sk, sq, err);
 }
 
 template <typename T, typename C>
 void read_t(const KvPoolArgs& p, const KvPlaceArgs& pl, const HeadsArgs& k, const HeadsArgs& v, int* err,
             cudaStream_t s) {
-  const Split sp = split_rows(pl.tokens, 2 * p.heads, p.dh / 16, 0);
+  const int chunks = p.dh / 16;
+  const Split sp = split_rows(pl.tokens, p.heads, chunks, 0, 2ll * pl.tokens * p.heads * chunks);
   const bool vec = aligned<T>(k) && aligned<T>(v);
-  launch_kernel(vec ? k_kv_read<T, C, true> : k_kv_read<T, C, false>, sp.blocks, kThreads, 0, s, p, pl, k, v, sp, err);
+  launch_kernel(vec ? k_kv_read<T, C, true> : k_kv_read<T, C, false>, 2 * sp.blocks, kThreads, 0, s, p, pl, k, v, sp, err);
 }
 
 }  // namespace
