@@ -61,22 +61,29 @@ Split split_rows(int n, int heads, int chunks, int rot, long long work) {
   return s;
 }
 
-// What a block does of it: tokens t0 .. t0 + n - 1, rows first .. end - 1 of
-// theirs for this thread, every `step`-th, part c of each.
+// What a block does of it: tokens t0 .. t0 + n - 1, rows lo .. end - 1 of
+// theirs, `step` at a time; this thread the `mine`-th of them, part c.  The
+// loops run alike in all threads and guard the accesses, so that whole warps
+// meet in the shuffles.
 struct Range {
-  int t0, n, first, end, step, c;
+  int t0, n, lo, end, step, mine, c;
 };
 __device__ __forceinline__ Range range_of(const Split& s, int block, int tokens) {
   Range r;
-  const int group = (int)div_fast((uint32_t)block, s.by_parts), lo = (block - group * s.parts) * s.span;
+  const int group = (int)div_fast((uint32_t)block, s.by_parts);
   r.t0 = group * s.tokens;
   r.n = min(s.tokens, tokens - r.t0);
   r.step = (int)div_fast(kThreads, s.by_chunks);
-  const int mine = (int)div_fast(threadIdx.x, s.by_chunks);
-  r.c = threadIdx.x - mine * s.chunks;
-  r.first = lo + mine;
-  r.end = mine < r.step ? min(r.n * s.heads, lo + s.span) : 0;
+  r.mine = (int)div_fast(threadIdx.x, s.by_chunks);
+  r.c = threadIdx.x - r.mine * s.chunks;
+  r.lo = (block - group * s.parts) * s.span;
+  r.end = min(r.n * s.heads, r.lo + s.span);
   return r;
+}
+// This thread's row of the group of rows from `lo` on; false: none.
+__device__ __forceinline__ bool row_at(const Range& r, int lo, int* i) {
+  *i = lo + r.mine;
+  return r.mine < r.step && *i < r.end;
 }
 struct Row {
   int token, head;  // token within the block
@@ -180,7 +187,7 @@ template <typename T> constexpr int kAhead = 4 / sizeof(T);
 
 // Blocks below sa.blocks take rows of a, the others of b.
 template <typename T, bool VEC>
-__global__ void __launch_bounds__(kThreads) k_rope(const RopeArgs r, const int* __restrict__ pos, int n, int dh,
+__global__ void __launch_bounds__(kThreads, 4) k_rope(const RopeArgs r, const int* __restrict__ pos, int n, int dh,
                                                    const HeadsArgs a, const HeadsArgs b, bool back, const Split sa,
                                                    const Split sb) {
   __shared__ __align__(16) float angles[kAnglesMax];
@@ -197,42 +204,42 @@ __global__ void __launch_bounds__(kThreads) k_rope(const RopeArgs r, const int* 
     int e0, e1;
     vectors_of(e0, e1, range.c, r.rot, dh);
     Raw8<T> x[U], y[U];
-    auto fetch = [&](int i0) {
+    auto fetch = [&](int lo) {
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const int i = i0 + u * range.step;
-        if (i >= range.end) continue;
-        const Row row = row_of(s, i);
-        const T* p = in + row.token * t.in_tok + row.head * t.in_head;
-        x[u].load(p + e0), y[u].load(p + e1);
+        int i;
+        if (row_at(range, lo + u * range.step, &i)) {
+          const Row row = row_of(s, i);
+          const T* p = in + row.token * t.in_tok + row.head * t.in_head;
+          x[u].load(p + e0), y[u].load(p + e1);
+        }
       }
     };
-    int i0 = range.first;
-    fetch(i0);
+    fetch(range.lo);
     fill_angles(angles, r, s, range, pos, back);
     __syncthreads();
-    while (i0 < range.end) {
+    for (int lo = range.lo; lo < range.end; lo += U * range.step) {
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const int i = i0 + u * range.step;
-        if (i >= range.end) continue;
-        const Row row = row_of(s, i);
-        float v[8], w[8];
-        x[u].get(v), y[u].get(w);
-        if (range.c < r.rot / 16) rotate16(v, w, range.c, angles + row.token * r.rot, r);
-        T* p = out + row.token * t.out_tok + row.head * t.out_head;
-        store8<true>(p + e0, v);
-        store8<true>(p + e1, w);
+        int i;
+        if (row_at(range, lo + u * range.step, &i)) {
+          const Row row = row_of(s, i);
+          float v[8], w[8];
+          x[u].get(v), y[u].get(w);
+          if (range.c < r.rot / 16) rotate16(v, w, range.c, angles + row.token * r.rot, r);
+          T* p = out + row.token * t.out_tok + row.head * t.out_head;
+          store8<true>(p + e0, v);
+          store8<true>(p + e1, w);
+        }
       }
-      i0 += U * range.step;
-      fetch(i0);
+      fetch(lo + U * range.step);
     }
   } else {
     fill_angles(angles, r, s, range, pos, back);
     __syncthreads();
     int e0, e1;
     pair_of(e0, e1, range.c, r);
-    for (int i = range.first; i < range.end; i += range.step) {
+    for (int i, lo = range.lo; row_at(range, lo, &i); lo += range.step) {
       const Row row = row_of(s, i);
       const T* p = in + row.token * t.in_tok + row.head * t.in_head;
       float x = ld_f(p + e0), y = ld_f(p + e1);
@@ -269,16 +276,14 @@ __device__ __forceinline__ void fill_places(Places& out, const KvPoolArgs& p, co
 // of `lanes` of the warp, at least two) agree on its scale.  `m` is the
 // largest of this thread's magnitudes as bits: the order of unsigned numbers
 // is that of magnitudes, with infinities and NaN above every number.  The
-// group's first thread divides for the scale, the others for the codes, in
-// one instruction sequence.
+// group's first thread divides for the scale, which is returned there, the
+// others for the codes, in one instruction sequence.
 template <typename C>
-__device__ __forceinline__ void quantise16(float (&x)[8], float (&y)[8], uint32_t m, float* scale, int lanes, bool first) {
-  const int lead = threadIdx.x & 31 & ~(lanes - 1);
-  const unsigned mask = ((1u << lanes) - 1) << lead;
-  for (int o = lanes / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(mask, m, o));
+__device__ __forceinline__ float quantise16(float (&x)[8], float (&y)[8], uint32_t m, int lanes, bool first) {
+  for (int o = lanes / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
   const float amax = fmaxf(__uint_as_float(m), 1e-30f), top = KvKind<C>::top;
   const float q = (first ? amax : top) / (first ? top : amax);
-  const float inv = __shfl_sync(mask, q, lead + 1);
+  const float inv = __shfl_sync(0xffffffffu, q, (threadIdx.x & 31 & ~(lanes - 1)) + 1);
   const bool fine = m < 0x7f800000u;
 #pragma unroll
   for (int i = 0; i < 8; ++i) x[i] *= inv, y[i] *= inv;
@@ -286,7 +291,7 @@ __device__ __forceinline__ void quantise16(float (&x)[8], float (&y)[8], uint32_
 #pragma unroll
     for (int i = 0; i < 8; ++i) x[i] = y[i] = 0.f;
   }
-  if (first) *scale = fine ? q : __uint_as_float(0x7fffffffu);
+  return fine ? q : __uint_as_float(0x7fffffffu);
 }
 __device__ __forceinline__ uint32_t largest(const float (&x)[8], const float (&y)[8]) {
   uint32_t m = 0;
@@ -305,7 +310,7 @@ __device__ __forceinline__ uint32_t largest(const Raw8<bf16>& x, const Raw8<bf16
 // Blocks below sk.blocks take key rows, as many after them value rows, the
 // others query rows, which are rotated into q.out.
 template <typename T, typename C, bool VEC>
-__global__ void __launch_bounds__(kThreads) k_kv_write(const KvPoolArgs p, const KvPlaceArgs pl, const HeadsArgs k,
+__global__ void __launch_bounds__(kThreads, 4) k_kv_write(const KvPoolArgs p, const KvPlaceArgs pl, const HeadsArgs k,
                                                        const HeadsArgs v, const RopeArgs r, const HeadsArgs q,
                                                        const Split sk, const Split sq, int* err) {
   __shared__ __align__(16) float angles[kAnglesMax];
@@ -323,20 +328,20 @@ __global__ void __launch_bounds__(kThreads) k_kv_write(const KvPoolArgs p, const
   Raw8<T> rx[U], ry[U];
   int e0 = 0, e1 = 0;
   if constexpr (VEC) vectors_of(e0, e1, range.c, r.rot, p.dh);
-  auto fetch = [&](int i0) {
+  auto fetch = [&](int lo) {
     if constexpr (VEC) {
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const int i = i0 + u * range.step;
-        if (i >= range.end) continue;
-        const Row row = row_of(s, i);
-        const T* from = in + row.token * t.in_tok + row.head * t.in_head;
-        rx[u].load(from + e0), ry[u].load(from + e1);
+        int i;
+        if (row_at(range, lo + u * range.step, &i)) {
+          const Row row = row_of(s, i);
+          const T* from = in + row.token * t.in_tok + row.head * t.in_head;
+          rx[u].load(from + e0), ry[u].load(from + e1);
+        }
       }
     }
   };
-  int i0 = range.first;
-  fetch(i0);
+  fetch(range.lo);
   if (turns) fill_angles(angles, r, s, range, pl.pos, false);
   if (query) {  // follows its position alone, whether or not its place exists
     for (int i = threadIdx.x; i < range.n; i += kThreads) places.at[i] = pl.pos[range.t0 + i] < 0 ? -1 : 0;
@@ -346,14 +351,14 @@ __global__ void __launch_bounds__(kThreads) k_kv_write(const KvPoolArgs p, const
   __syncthreads();
   C* const pages = (C*)(value ? p.v : p.k);
   float* const scales = value ? p.v_scale : p.k_scale;
-  while (i0 < range.end) {
+  for (int lo = range.lo; lo < range.end; lo += U * range.step) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int i = i0 + u * range.step;
-      if (i >= range.end) continue;
-      const Row row = row_of(s, i);
+      int i;
+      const bool mine = row_at(range, lo + u * range.step, &i);
+      const Row row = row_of(s, mine ? i : 0);
       const long long at = places.at[row.token];
-      if (at < 0) continue;
+      const bool ok = mine && at >= 0;
       float x[8], y[8];
       const float* f = angles + row.token * r.rot;
       if constexpr (VEC) {
@@ -372,37 +377,37 @@ __global__ void __launch_bounds__(kThreads) k_kv_write(const KvPoolArgs p, const
       if (query) {
         T* out = (T*)q.out + (range.t0 + row.token) * q.out_tok + row.head * q.out_head;
         if constexpr (VEC) {
-          store8<true>(out + e0, x), store8<true>(out + e1, y);
+          if (ok) store8<true>(out + e0, x), store8<true>(out + e1, y);
         } else {
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
             pair_of(e0, e1, 8 * range.c + j, r);
-            st_f(out + e0, x[j]), st_f(out + e1, y[j]);
+            if (ok) st_f(out + e0, x[j]), st_f(out + e1, y[j]);
           }
         }
-        continue;
-      }
-      if constexpr (KvKind<C>::narrow) {
-        uint32_t m;
-        if constexpr (VEC && sizeof(T) == 2)
-          m = turns ? largest(x, y) : largest(rx[u], ry[u]);
-        else
-          m = largest(x, y);
-        quantise16<C>(x, y, m, scales + places.scale[row.token] + row.head * p.scale_head, s.chunks, range.c == 0);
-      }
-      C* out = pages + at + row.head * p.head;
-      if constexpr (VEC) {
-        store8<true>(out + e0, x), store8<true>(out + e1, y);
       } else {
+        if constexpr (KvKind<C>::narrow) {
+          uint32_t m;
+          if constexpr (VEC && sizeof(T) == 2)
+            m = turns ? largest(x, y) : largest(rx[u], ry[u]);
+          else
+            m = largest(x, y);
+          const float scale = quantise16<C>(x, y, m, s.chunks, range.c == 0);
+          if (ok && range.c == 0) scales[places.scale[row.token] + row.head * p.scale_head] = scale;
+        }
+        C* out = pages + at + row.head * p.head;
+        if constexpr (VEC) {
+          if (ok) store8<true>(out + e0, x), store8<true>(out + e1, y);
+        } else {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          pair_of(e0, e1, 8 * range.c + j, r);
-          store1(out + e0, x[j]), store1(out + e1, y[j]);
+          for (int j = 0; j < 8; ++j) {
+            pair_of(e0, e1, 8 * range.c + j, r);
+            if (ok) store1(out + e0, x[j]), store1(out + e1, y[j]);
+          }
         }
       }
     }
-    i0 += U * range.step;
-    fetch(i0);
+    fetch(lo + U * range.step);
   }
 }
 
@@ -422,32 +427,34 @@ __global__ void __launch_bounds__(kThreads) k_kv_read(const KvPoolArgs p, const 
   const C* const pages = (const C*)(value ? p.v : p.k) + 8 * range.c;
   const float* const scales = value ? p.v_scale : p.k_scale;
   T* const base = (T*)t.out + range.t0 * t.out_tok + 8 * range.c;
-  for (int i0 = range.first; i0 < range.end; i0 += U * range.step) {
+  for (int lo = range.lo; lo < range.end; lo += U * range.step) {
     Raw8<C> rx[U], ry[U];
     float scale[U];
+    T* out[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      if (i0 + u * range.step >= range.end) continue;
-      const Row row = row_of(s, i0 + u * range.step);
+      int i;
+      const bool mine = row_at(range, lo + u * range.step, &i);
+      const Row row = row_of(s, mine ? i : 0);
       const long long at = places.at[row.token];
-      if (at < 0) continue;
-      const C* in = pages + at + row.head * p.head;
-      rx[u].load(in), ry[u].load(in + p.dh / 2);
-      if constexpr (KvKind<C>::narrow) scale[u] = scales[places.scale[row.token] + row.head * p.scale_head];
+      out[u] = nullptr;
+      if (mine && at >= 0) {
+        out[u] = base + row.token * t.out_tok + row.head * t.out_head;
+        const C* in = pages + at + row.head * p.head;
+        rx[u].load(in), ry[u].load(in + p.dh / 2);
+        if constexpr (KvKind<C>::narrow) scale[u] = scales[places.scale[row.token] + row.head * p.scale_head];
+      }
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      if (i0 + u * range.step >= range.end) continue;
-      const Row row = row_of(s, i0 + u * range.step);
-      if (places.at[row.token] < 0) continue;
+      if (!out[u]) continue;
       float x[8], y[8];
       rx[u].get(x), ry[u].get(y);
       if constexpr (KvKind<C>::narrow) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) x[j] *= scale[u], y[j] *= scale[u];
       }
-      T* out = base + row.token * t.out_tok + row.head * t.out_head;
-      store8<VEC>(out, x), store8<VEC>(out + p.dh / 2, y);
+      store8<VEC>(out[u], x), store8<VEC>(out[u] + p.dh / 2, y);
     }
   }
 }
