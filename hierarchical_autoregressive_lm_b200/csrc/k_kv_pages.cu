@@ -185,18 +185,12 @@ template <typename T> struct Raw8 {
 // Rows a thread has in flight: 64 bytes of its parts.
 template <typename T> constexpr int kAhead = 4 / sizeof(T);
 
-// Blocks below sa.blocks take rows of a, the others of b.
+// A block's rows of one tensor, rotated.  Padding tokens (negative positions)
+// are left out if `padded`.
 template <typename T, bool VEC>
-__global__ void __launch_bounds__(kThreads, 4) k_rope(const RopeArgs r, const int* __restrict__ pos, int n, int dh,
-                                                   const HeadsArgs a, const HeadsArgs b, bool back, const Split sa,
-                                                   const Split sb) {
-  __shared__ __align__(16) float angles[kAnglesMax];
-  pdl_wait();
-  pdl_trigger();
-  const bool second = (int)blockIdx.x >= sa.blocks;
-  const Split s = second ? sb : sa;
-  const HeadsArgs t = second ? b : a;
-  const Range range = range_of(s, second ? blockIdx.x - sa.blocks : blockIdx.x, n);
+__device__ __forceinline__ void rotate_rows(float* angles, const RopeArgs& r, const int* pos, int n, int dh,
+                                            const HeadsArgs& t, const Split& s, int block, bool back, bool padded) {
+  const Range range = range_of(s, block, n);
   const T* const in = (const T*)t.in + range.t0 * t.in_tok;
   T* const out = (T*)t.out + range.t0 * t.out_tok;
   if constexpr (VEC) {
@@ -222,33 +216,52 @@ __global__ void __launch_bounds__(kThreads, 4) k_rope(const RopeArgs r, const in
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         int i;
-        if (row_at(range, lo + u * range.step, &i)) {
-          const Row row = row_of(s, i);
-          float v[8], w[8];
-          x[u].get(v), y[u].get(w);
-          if (range.c < r.rot / 16) rotate16(v, w, range.c, angles + row.token * r.rot, r);
-          T* p = out + row.token * t.out_tok + row.head * t.out_head;
-          store8<true>(p + e0, v);
-          store8<true>(p + e1, w);
-        }
+        if (!row_at(range, lo + u * range.step, &i)) continue;
+        const Row row = row_of(s, i);
+        if (padded && pos[range.t0 + row.token] < 0) continue;
+        float v[8], w[8];
+        x[u].get(v), y[u].get(w);
+        if (range.c < r.rot / 16) rotate16(v, w, range.c, angles + row.token * r.rot, r);
+        T* p = out + row.token * t.out_tok + row.head * t.out_head;
+        store8<true>(p + e0, v);
+        store8<true>(p + e1, w);
       }
       fetch(lo + U * range.step);
     }
   } else {
     fill_angles(angles, r, s, range, pos, back);
     __syncthreads();
-    int e0, e1;
-    pair_of(e0, e1, range.c, r);
-    for (int i, lo = range.lo; row_at(range, lo, &i); lo += range.step) {
+    for (int lo = range.lo; lo < range.end; lo += range.step) {
+      int i;
+      if (!row_at(range, lo, &i)) continue;
       const Row row = row_of(s, i);
+      if (padded && pos[range.t0 + row.token] < 0) continue;
       const T* p = in + row.token * t.in_tok + row.head * t.in_head;
-      float x = ld_f(p + e0), y = ld_f(p + e1);
-      const float* f = angles + row.token * r.rot + range.c;
-      if (range.c < r.rot / 2) rotate(x, y, f[0], f[r.rot / 2]);
       T* o = out + row.token * t.out_tok + row.head * t.out_head;
-      st_f(o + e0, x), st_f(o + e1, y);
+      for (int pair = range.c; pair < dh / 2; pair += s.chunks) {
+        int e0, e1;
+        pair_of(e0, e1, pair, r);
+        float x = ld_f(p + e0), y = ld_f(p + e1);
+        const float* f = angles + row.token * r.rot + pair;
+        if (pair < r.rot / 2) rotate(x, y, f[0], f[r.rot / 2]);
+        st_f(o + e0, x), st_f(o + e1, y);
+      }
     }
   }
+}
+
+// Blocks below sa.blocks take rows of a, the others of b.
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(kThreads, 4) k_rope(const RopeArgs r, const int* __restrict__ pos, int n, int dh,
+                                                      const HeadsArgs a, const HeadsArgs b, bool back, const Split sa,
+                                                      const Split sb) {
+  __shared__ __align__(16) float angles[kAnglesMax];
+  pdl_wait();
+  pdl_trigger();
+  if ((int)blockIdx.x < sa.blocks)
+    rotate_rows<T, VEC>(angles, r, pos, n, dh, a, sa, blockIdx.x, back, false);
+  else
+    rotate_rows<T, VEC>(angles, r, pos, n, dh, b, sb, blockIdx.x - sa.blocks, back, false);
 }
 
 // Where the block's tokens go: element and scale offsets, -1 for padding and
@@ -307,107 +320,85 @@ __device__ __forceinline__ uint32_t largest(const Raw8<bf16>& x, const Raw8<bf16
   return max(m << 16, m & 0xffff0000u);
 }
 
-// Blocks below sk.blocks take key rows, as many after them value rows, the
-// others query rows, which are rotated into q.out.
-template <typename T, typename C, bool VEC>
+// Blocks below sk.blocks take rows of k and v, which share a place, the
+// others rows of q, which are rotated into q.out.
+template <typename T, typename C, bool VEC, bool ROPE>
 __global__ void __launch_bounds__(kThreads, 4) k_kv_write(const KvPoolArgs p, const KvPlaceArgs pl, const HeadsArgs k,
-                                                       const HeadsArgs v, const RopeArgs r, const HeadsArgs q,
-                                                       const Split sk, const Split sq, int* err) {
-  __shared__ __align__(16) float angles[kAnglesMax];
+                                                          const HeadsArgs v, const RopeArgs r, const HeadsArgs q,
+                                                          const Split sk, const Split sq, int* err) {
+  __shared__ __align__(16) float angles[ROPE ? kAnglesMax : 1];
   __shared__ Places places;
   pdl_wait();
   pdl_trigger();
-  const bool query = (int)blockIdx.x >= 2 * sk.blocks, value = !query && (int)blockIdx.x >= sk.blocks;
-  const int block = blockIdx.x - (query ? 2 : value ? 1 : 0) * sk.blocks;
-  const Split s = query ? sq : sk;
-  const HeadsArgs t = query ? q : value ? v : k;
-  const Range range = range_of(s, block, pl.tokens);
-  const T* const in = (const T*)t.in + range.t0 * t.in_tok;
-  const bool turns = r.rot > 0 && !value;
-  constexpr int U = VEC ? kAhead<T> : 1;
-  Raw8<T> rx[U], ry[U];
+  if (ROPE && (int)blockIdx.x >= sk.blocks) {
+    rotate_rows<T, VEC>(angles, r, pl.pos, pl.tokens, p.dh, q, sq, blockIdx.x - sk.blocks, false, true);
+    return;
+  }
+  const Range range = range_of(sk, blockIdx.x, pl.tokens);
+  const T* const k_in = (const T*)k.in + range.t0 * k.in_tok;
+  const T* const v_in = (const T*)v.in + range.t0 * v.in_tok;
+  Raw8<T> raw[4];
   int e0 = 0, e1 = 0;
   if constexpr (VEC) vectors_of(e0, e1, range.c, r.rot, p.dh);
   auto fetch = [&](int lo) {
-    if constexpr (VEC) {
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        int i;
-        if (row_at(range, lo + u * range.step, &i)) {
-          const Row row = row_of(s, i);
-          const T* from = in + row.token * t.in_tok + row.head * t.in_head;
-          rx[u].load(from + e0), ry[u].load(from + e1);
-        }
-      }
+    int i;
+    if (VEC && row_at(range, lo, &i)) {
+      const Row row = row_of(sk, i);
+      const T* from = k_in + row.token * k.in_tok + row.head * k.in_head;
+      raw[0].load(from + e0), raw[1].load(from + e1);
+      from = v_in + row.token * v.in_tok + row.head * v.in_head;
+      raw[2].load(from + e0), raw[3].load(from + e1);
     }
   };
   fetch(range.lo);
-  if (turns) fill_angles(angles, r, s, range, pl.pos, false);
-  if (query) {  // follows its position alone, whether or not its place exists
-    for (int i = threadIdx.x; i < range.n; i += kThreads) places.at[i] = pl.pos[range.t0 + i] < 0 ? -1 : 0;
-  } else {
-    fill_places(places, p, pl, range, err);
-  }
+  if constexpr (ROPE) fill_angles(angles, r, sk, range, pl.pos, false);
+  fill_places(places, p, pl, range, err);
   __syncthreads();
-  C* const pages = (C*)(value ? p.v : p.k);
-  float* const scales = value ? p.v_scale : p.k_scale;
-  for (int lo = range.lo; lo < range.end; lo += U * range.step) {
+  for (int lo = range.lo; lo < range.end; lo += range.step) {
+    int i;
+    const bool mine = row_at(range, lo, &i);
+    const Row row = row_of(sk, mine ? i : 0);
+    const long long at = places.at[row.token];
+    const bool ok = mine && at >= 0;
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      int i;
-      const bool mine = row_at(range, lo + u * range.step, &i);
-      const Row row = row_of(s, mine ? i : 0);
-      const long long at = places.at[row.token];
-      const bool ok = mine && at >= 0;
+    for (int n = 0; n < 2; ++n) {  // k, v
       float x[8], y[8];
       const float* f = angles + row.token * r.rot;
       if constexpr (VEC) {
-        rx[u].get(x), ry[u].get(y);
-        if (turns && range.c < r.rot / 16) rotate16(x, y, range.c, f, r);
+        raw[2 * n].get(x), raw[2 * n + 1].get(y);
+        if (ROPE && n == 0 && range.c < r.rot / 16) rotate16(x, y, range.c, f, r);
       } else {
-        const T* from = in + row.token * t.in_tok + row.head * t.in_head;
+        const T* from = n ? v_in + row.token * v.in_tok + row.head * v.in_head
+                          : k_in + row.token * k.in_tok + row.head * k.in_head;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           const int pair = 8 * range.c + j;
           pair_of(e0, e1, pair, r);
           x[j] = ld_f(from + e0), y[j] = ld_f(from + e1);
-          if (turns && pair < r.rot / 2) rotate(x[j], y[j], f[pair], f[r.rot / 2 + pair]);
+          if (ROPE && n == 0 && pair < r.rot / 2) rotate(x[j], y[j], f[pair], f[r.rot / 2 + pair]);
         }
       }
-      if (query) {
-        T* out = (T*)q.out + (range.t0 + row.token) * q.out_tok + row.head * q.out_head;
-        if constexpr (VEC) {
-          if (ok) store8<true>(out + e0, x), store8<true>(out + e1, y);
-        } else {
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            pair_of(e0, e1, 8 * range.c + j, r);
-            if (ok) st_f(out + e0, x[j]), st_f(out + e1, y[j]);
-          }
-        }
+      if constexpr (KvKind<C>::narrow) {
+        uint32_t m;
+        if constexpr (VEC && sizeof(T) == 2)
+          m = ROPE && n == 0 ? largest(x, y) : largest(raw[2 * n], raw[2 * n + 1]);
+        else
+          m = largest(x, y);
+        const float scale = quantise16<C>(x, y, m, sk.chunks, range.c == 0);
+        if (ok && range.c == 0) (n ? p.v_scale : p.k_scale)[places.scale[row.token] + row.head * p.scale_head] = scale;
+      }
+      C* out = (C*)(n ? p.v : p.k) + at + row.head * p.head;
+      if constexpr (VEC) {
+        if (ok) store8<true>(out + e0, x), store8<true>(out + e1, y);
       } else {
-        if constexpr (KvKind<C>::narrow) {
-          uint32_t m;
-          if constexpr (VEC && sizeof(T) == 2)
-            m = turns ? largest(x, y) : largest(rx[u], ry[u]);
-          else
-            m = largest(x, y);
-          const float scale = quantise16<C>(x, y, m, s.chunks, range.c == 0);
-          if (ok && range.c == 0) scales[places.scale[row.token] + row.head * p.scale_head] = scale;
-        }
-        C* out = pages + at + row.head * p.head;
-        if constexpr (VEC) {
-          if (ok) store8<true>(out + e0, x), store8<true>(out + e1, y);
-        } else {
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            pair_of(e0, e1, 8 * range.c + j, r);
-            if (ok) store1(out + e0, x[j]), store1(out + e1, y[j]);
-          }
+        for (int j = 0; j < 8; ++j) {
+          pair_of(e0, e1, 8 * range.c + j, r);
+          if (ok) store1(out + e0, x[j]), store1(out + e1, y[j]);
         }
       }
     }
-    fetch(lo + U * range.step);
+    fetch(lo + range.step);
   }
 }
 
@@ -476,11 +467,14 @@ bool rope_vectors(const RopeArgs& r, int dh, const HeadsArgs& a, const HeadsArgs
   return r.rot % 16 == 0 && dh % 16 == 0 && aligned<T>(a) && aligned<T>(b);
 }
 
+// Threads of a row: of 16 elements each in vectors, else of a pair at a time.
+inline int rope_chunks(bool vec, int dh) { return vec ? dh / 16 : dh / 2 < 32 ? dh / 2 : 32; }
+
 template <typename T>
 void rope_t(const RopeArgs& r, const int* pos, int n, int dh, const HeadsArgs& a, const HeadsArgs& b, bool back,
             cudaStream_t s) {
   const bool vec = rope_vectors<T>(r, dh, a, b);
-  const int chunks = vec ? dh / 16 : dh / 2;
+  const int chunks = rope_chunks(vec, dh);
   const long long work = (long long)n * (a.heads + b.heads) * chunks;
   const Split sa = split_rows(n, a.heads, chunks, r.rot, work);
   const Split sb = b.heads ? split_rows(n, b.heads, chunks, r.rot, work) : Split();
@@ -492,14 +486,15 @@ template <typename T, typename C>
 void write_t(const KvPoolArgs& p, const KvPlaceArgs& pl, const HeadsArgs& k, const HeadsArgs& v, const RopeArgs* r,
              const HeadsArgs& q, int* err, cudaStream_t s) {
   const RopeArgs rope = r ? *r : RopeArgs();
-  const int chunks = p.dh / 16;
-  const long long work = (long long)pl.tokens * (2 * p.heads + q.heads) * chunks;
-  const Split sk = split_rows(pl.tokens, p.heads, chunks, rope.rot, work);
-  const Split sq = q.heads ? split_rows(pl.tokens, q.heads, chunks, rope.rot, work) : Split();
   // one choice for the whole launch: rows of k, v and q all in vectors, or none
   const bool vec = aligned<T>(k) && rope_vectors<T>(rope, p.dh, v, q);
-  launch_kernel(vec ? k_kv_write<T, C, true> : k_kv_write<T, C, false>, 2 * sk.blocks + sq.blocks, kThreads, 0, s, p,
-                pl, k, v, rope, q, sk, sq, err);
+  const int chunks = p.dh / 16, q_chunks = rope_chunks(vec, p.dh);
+  const long long work = (long long)pl.tokens * (2ll * p.heads * chunks + (long long)q.heads * q_chunks);
+  const Split sk = split_rows(pl.tokens, p.heads, chunks, rope.rot, work);
+  const Split sq = q.heads ? split_rows(pl.tokens, q.heads, q_chunks, rope.rot, work) : Split();
+  auto* kernel = rope.rot ? (vec ? k_kv_write<T, C, true, true> : k_kv_write<T, C, false, true>)
+                          : (vec ? k_kv_write<T, C, true, false> : k_kv_write<T, C, false, false>);
+  launch_kernel(kernel, sk.blocks + sq.blocks, kThreads, 0, s, p, pl, k, v, rope, q, sk, sq, err);
 }
 
 template <typename T, typename C>
