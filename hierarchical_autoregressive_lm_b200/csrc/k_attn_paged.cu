@@ -11,13 +11,15 @@
 // heads of a unit, so the kernel is bound by the cache's bytes; 4 flops per
 // element and head are far below what the tensor cores take.
 //
-// Split.  Lengths live on the device, so the host cannot deal them out.  One
-// CTA per resident slot takes an equal share of all steps of all units, in
-// unit order, from a prefix sum over the lengths: every CTA reads the same
-// number of rows, however uneven the sequences.  A unit that falls into
-// several CTAs leaves parts (accumulator, maximum, sum), which a second
-// kernel joins in the order of the positions.  Calls with few steps or many
-// units run one CTA per unit instead, without parts.
+// Split.  Lengths live on the device, so the host cannot deal them out.
+//  * Shares: one CTA per resident slot takes an equal share of all steps of
+//    all units, in unit order, from a prefix sum over the lengths: every CTA
+//    reads the same number of rows, however uneven the sequences.  A unit that
+//    falls into several CTAs leaves parts (accumulator, maximum, sum), which a
+//    second kernel joins in the order of the positions.
+//  * Clusters: a thread-block cluster of one to eight CTAs divides each unit
+//    and joins it through distributed shared memory: one launch, no scratch.
+// Which one a call takes: see choose().
 #include <cmath>
 #include <type_traits>
 
@@ -32,12 +34,14 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kHeadsMax = 8;  // query heads of a unit
+constexpr int kClusterMax = 8;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 // How a launch deals out its work; parts are [cta][2][kHeadsMax].
 struct Plan {
   int chunks, gh;  // units per key head, query heads of each
-  int ctas;        // 0: one CTA per unit
+  int ctas;        // 0: a cluster per unit
+  int cluster;
   int min_steps;   // least steps worth a CTA
   float* acc;      // [cta][2][kHeadsMax][D]
   float2* ml;      // maximum and sum
@@ -57,21 +61,21 @@ __device__ __forceinline__ void cp_wait() {
 }
 __device__ __forceinline__ void ldsm(uint32_t (&r)[4], uint32_t a) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a) : "memory");
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a));
 }
 __device__ __forceinline__ void ldsm_t(uint32_t (&r)[4], uint32_t a) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a) : "memory");
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a));
 }
 // c[16 x 8] += a[16 x 16] b[16 x 8], fp32 accumulators.
 __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                     uint32_t b1, bf16) {
-  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3]) : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                     uint32_t b1, __half) {
-  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3]) : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
@@ -119,6 +123,13 @@ struct Joint {
   float m[kWarps][kHeadsMax], l[kWarps][kHeadsMax];
 };
 
+// The same of a whole CTA, for the other CTAs of its cluster.
+template <int D>
+struct Joined {
+  float o[kHeadsMax][D];
+  float m[kHeadsMax], l[kHeadsMax];
+};
+
 // bf16 queries on the tensor cores (m16n8k16: with eight query heads, one
 // token each, larger tiles would stay empty; the cache's bytes are the bound).
 //
@@ -149,7 +160,7 @@ struct TensorCores {
   static constexpr int kWarpBytes = kStages * kStage;
   static constexpr int kSmem = kWarps * kWarpBytes;
   static constexpr int kCtas = 2 * kSmem <= 220 * 1024 ? 2 : 1;
-  static_assert(kSmem >= (int)sizeof(Joint<D>) && kTile % 128 == 0, "the ring is reused for the join");
+  static_assert(kSmem >= (int)(sizeof(Joint<D>) + sizeof(Joined<D>)) && kTile % 128 == 0, "the ring is reused for the join");
   static constexpr int KS = D / 16;   // k steps of the first product
   static constexpr int NT = D / 8;    // column tiles of the second
   static constexpr int SUB = TP / 16;
@@ -441,6 +452,7 @@ struct CudaCores {
   static constexpr int kCtas = 2;
   struct Shared {
     Joint<D> joint;
+    Joined<D> joined;
     float q[GH][D];
     float p[kWarps][TP][GH];
     long long off[kWarps][TP];
@@ -619,31 +631,72 @@ __device__ __forceinline__ void share_of(const PagedAttnArgs& a, const Plan& pla
   __syncthreads();
 }
 
-// The warps' results joined, as a unit's output (slot < 0) or as a part.
+// Element e of head h over n results of the same unit, as accumulator,
+// maximum and sum; get(k, &m, &l, &o) fetches the k-th.
+struct Total {
+  float o, m, l;
+};
+template <int N, typename F>
+__device__ __forceinline__ Total total_of(int n, F&& get) {
+  float m[N], l[N], o[N];
+  Total t = {0.f, -INFINITY, 0.f};
+#pragma unroll
+  for (int k = 0; k < N; ++k)
+    if (k < n) get(k, m[k], l[k], o[k]), t.m = fmaxf(t.m, m[k]);
+  const float base = t.m == -INFINITY ? 0.f : t.m;
+#pragma unroll
+  for (int k = 0; k < N; ++k)
+    if (k < n) {
+      const float f = exp2f(m[k] - base);
+      t.l += f * l[k];
+      t.o += f * o[k];
+    }
+  return t;
+}
+template <int D>
+__device__ __forceinline__ Total over_warps(const Joint<D>& joint, int h, int e) {
+  return total_of<kWarps>(kWarps, [&](int k, float& m, float& l, float& o) {
+    m = joint.m[k][h], l = joint.l[k][h], o = joint.o[k][h][e];
+  });
+}
+template <class E>
+__device__ __forceinline__ void put(const PagedAttnArgs& a, const Unit& u, int h, int e, const Total& t) {
+  st_f((typename E::T*)a.o + u.b * a.o_seq + (u.h0 + h) * a.o_head + e, t.l == 0.f ? 0.f : t.o / t.l);
+  if (a.lse && e == 0)
+    a.lse[(long long)u.b * a.q_heads + u.h0 + h] =
+        t.l == 0.f ? -INFINITY : ((t.m == -INFINITY ? 0.f : t.m) + log2f(t.l)) * kLn2;
+}
+// The cluster's CTAs have attended to a unit: each writes its share of the outputs.
 template <class E, int D>
-__device__ __forceinline__ void put(const PagedAttnArgs& a, const Plan& plan, const Unit& u, const Joint<D>& joint,
-                                    long long slot) {
+__device__ __forceinline__ void put_cluster(const PagedAttnArgs& a, const Unit& u, const Joint<D>& joint, Joined<D>& mine,
+                                            int rank, int ranks) {
   for (int i = threadIdx.x; i < u.nh * D; i += kThreads) {
     const int h = i / D, e = i % D;
-    float mx = joint.m[0][h], sum = 0.f, o = 0.f;
-#pragma unroll
-    for (int k = 1; k < kWarps; ++k) mx = fmaxf(mx, joint.m[k][h]);
-    const float base = mx == -INFINITY ? 0.f : mx;
-#pragma unroll
-    for (int k = 0; k < kWarps; ++k) {
-      const float f = exp2f(joint.m[k][h] - base);
-      sum += f * joint.l[k][h];
-      o += f * joint.o[k][h][e];
-    }
-    if (slot < 0) {
-      st_f((typename E::T*)a.o + u.b * a.o_seq + (u.h0 + h) * a.o_head + e, sum == 0.f ? 0.f : o / sum);
-      if (a.lse && e == 0)
-        a.lse[(long long)u.b * a.q_heads + u.h0 + h] = sum == 0.f ? -INFINITY : (base + log2f(sum)) * kLn2;
-    } else {
-      plan.acc[(slot * kHeadsMax + h) * D + e] = o;
-      if (e == 0) plan.ml[slot * kHeadsMax + h] = make_float2(mx, sum);
-    }
+    const Total t = over_warps(joint, h, e);
+    mine.o[h][e] = t.o;
+    if (e == 0) mine.m[h] = t.m, mine.l[h] = t.l;
   }
+  ptx::cluster_sync();
+  const uint32_t o = ptx::smem_u32(mine.o), m = ptx::smem_u32(mine.m), l = ptx::smem_u32(mine.l);
+  for (int i = rank * kThreads + threadIdx.x; i < u.nh * D; i += ranks * kThreads) {
+    const int h = i / D, e = i % D;
+    put<E>(a, u, h, e, total_of<kClusterMax>(ranks, [&](int k, float& pm, float& pl, float& po) {
+      pm = ptx::ld_shared_cluster_f32(ptx::map_shared_rank(m + 4 * h, k));
+      pl = ptx::ld_shared_cluster_f32(ptx::map_shared_rank(l + 4 * h, k));
+      po = ptx::ld_shared_cluster_f32(ptx::map_shared_rank(o + 4 * i, k));
+    }));
+  }
+  ptx::cluster_sync();  // no CTA leaves while others read its shared memory
+}
+
+__device__ __forceinline__ Unit unit_of(const PagedAttnArgs& a, const Plan& plan, int b, int unit, int* err) {
+  const int group = a.q_heads / a.pool.heads, skip = unit % plan.chunks * plan.gh;
+  Unit u;
+  u.b = b, u.kh = unit / plan.chunks;
+  u.h0 = u.kh * group + skip, u.nh = min(plan.gh, group - skip);
+  u.len = length_of(a, b, err), u.first = first_of(a, u.len);
+  u.table = a.table + b * a.table_stride;
+  return u;
 }
 
 template <class E, int D>
@@ -652,39 +705,45 @@ __global__ void __launch_bounds__(kThreads, E::kCtas) k_attn_paged(const PagedAt
   __shared__ Share share;
   pdl_wait();
   pdl_trigger();
-  const int units = a.pool.heads * plan.chunks, group = a.q_heads / a.pool.heads;
-  int b, unit, step;
-  long long left;
+  const int units = a.pool.heads * plan.chunks;
+  const Joint<D>& joint = *reinterpret_cast<const Joint<D>*>(smem);
   if (plan.ctas == 0) {
-    b = blockIdx.x / units, unit = blockIdx.x % units, step = 0, left = 1ll << 40;
-  } else {
-    share_of<E::kStep>(a, plan, blockIdx.x, &share);
-    if (threadIdx.x == 0) plan.meta[blockIdx.x] = make_int4(0, 0, -1, 0);
-    b = share.b, unit = share.unit, step = share.step, left = share.steps;
+    const int at = blockIdx.x / plan.cluster, rank = blockIdx.x % plan.cluster;
+    const Unit u = unit_of(a, plan, at / units, at % units, err);
+    const int steps = (u.len - u.first + E::kStep - 1) / E::kStep;
+    const int s0 = (int)((long long)steps * rank / plan.cluster), s1 = (int)((long long)steps * (rank + 1) / plan.cluster);
+    E::run(a, u, u.first + s0 * E::kStep, min(u.len, u.first + s1 * E::kStep), smem, err);
+    if (plan.cluster > 1) {
+      put_cluster<E, D>(a, u, joint, *reinterpret_cast<Joined<D>*>(smem + sizeof(Joint<D>)), rank, plan.cluster);
+    } else {
+      for (int i = threadIdx.x; i < u.nh * D; i += kThreads) put<E>(a, u, i / D, i % D, over_warps(joint, i / D, i % D));
+    }
+    return;
   }
-  while (left > 0) {
-    Unit u;
-    u.b = b, u.kh = unit / plan.chunks;
-    const int skip = unit % plan.chunks * plan.gh;
-    u.h0 = u.kh * group + skip, u.nh = min(plan.gh, group - skip);
-    u.len = length_of(a, b, err), u.first = first_of(a, u.len);
-    u.table = a.table + b * a.table_stride;
+  share_of<E::kStep>(a, plan, blockIdx.x, &share);
+  if (threadIdx.x == 0) plan.meta[blockIdx.x] = make_int4(0, 0, -1, 0);
+  int b = share.b, unit = share.unit, step = share.step;
+  for (long long left = share.steps; left > 0;) {
+    const Unit u = unit_of(a, plan, b, unit, err);
     const int steps = max(1, (u.len - u.first + E::kStep - 1) / E::kStep);
     const int n = (int)min((long long)(steps - step), left);
-    const int p0 = u.first + step * E::kStep;
-    const int p1 = n < steps - step ? p0 + n * E::kStep : u.len;
-    E::run(a, u, p0, p1, smem, err);
-    long long slot = -1;
-    if (n < steps) {
-      slot = blockIdx.x * 2ll + (step == 0);
-      if (step == 0 && threadIdx.x == 0) {
-        // the unit's last step is the (x + 1)-th of all, x + 1 - its share's start = steps
-        const long long start = (long long)blockIdx.x * share.all / share.ctas + (share.steps - left);
-        plan.meta[blockIdx.x] = make_int4(b, unit, (int)(((start + steps) * share.ctas - 1) / share.all), 0);
+    E::run(a, u, u.first + step * E::kStep, n < steps - step ? u.first + (step + n) * E::kStep : u.len, smem, err);
+    const long long slot = blockIdx.x * 2ll + (step == 0);
+    if (n < steps && step == 0 && threadIdx.x == 0) {
+      // steps up to and with the unit's last: they end in the share that holds it
+      const long long upto = (long long)blockIdx.x * share.all / share.ctas + (share.steps - left) + steps;
+      plan.meta[blockIdx.x] = make_int4(b, unit, (int)((upto * share.ctas - 1) / share.all), 0);
+    }
+    for (int i = threadIdx.x; i < u.nh * D; i += kThreads) {
+      const int h = i / D, e = i % D;
+      const Total t = over_warps(joint, h, e);
+      if (n == steps) {
+        put<E>(a, u, h, e, t);
+      } else {
+        plan.acc[(slot * kHeadsMax + h) * D + e] = t.o;
+        if (e == 0) plan.ml[slot * kHeadsMax + h] = make_float2(t.m, t.l);
       }
     }
-    put<E, D>(a, plan, u, *reinterpret_cast<const Joint<D>*>(smem), slot);
-    if (plan.ctas == 0) break;
     left -= n, step = 0;
     if (++unit == units) unit = 0, ++b;
     __syncthreads();
@@ -742,19 +801,45 @@ __global__ void __launch_bounds__(kJoinThreads) k_attn_join(const PagedAttnArgs 
 
 // ------------------------------------------------------------------ host
 
-// CTAs of k_attn_paged<E, D> that the current device holds at once.
+// Clusters of 2^log2 CTAs of k_attn_paged<E, D> that the current device holds at once.
 template <class E, int D>
-int resident_ctas() {
-  static PerDevice cache;
-  return cache.get([] {
-    int per_sm = 0;
+int resident(int log2) {
+  static PerDevice cache[4];
+  return cache[log2].get([=] {
     cudaFuncSetAttribute(k_attn_paged<E, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, E::kSmem);
-    cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, k_attn_paged<E, D>, kThreads, E::kSmem);
-    return device_sm_count() * (per_sm > 0 ? per_sm : 1);
+    int n = 0;
+    if (log2 == 0) {
+      cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, k_attn_paged<E, D>, kThreads, E::kSmem);
+      n *= device_sm_count();
+    } else {
+      cudaLaunchConfig_t cfg = {};
+      cudaLaunchAttribute attr;
+      attr.id = cudaLaunchAttributeClusterDimension;
+      attr.val.clusterDim.x = 1 << log2;
+      attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+      cfg.gridDim = dim3(1 << log2), cfg.blockDim = dim3(kThreads), cfg.dynamicSmemBytes = E::kSmem;
+      cfg.attrs = &attr, cfg.numAttrs = 1;
+      if (cudaOccupancyMaxActiveClusters(&n, k_attn_paged<E, D>, &cfg) != cudaSuccess) n = 0, cudaGetLastError();
+    }
+    return n > 0 ? n : log2 == 0 ? 1 : 0;
   });
 }
 
-constexpr int kMinSteps = 2;
+constexpr int kMinSteps = 2;   // of a share
+constexpr int kJoinSteps = 8;  // what shares cost beyond their steps
+
+// Sets plan.cluster, and plan.ctas where shares are better.
+template <class E, int D>
+void choose(Plan& plan, long long units, long long steps) {
+  int log2 = 0;
+  while (log2 < 3 && (2 << log2) <= steps && units <= resident<E, D>(log2 + 1)) ++log2;
+  const int slots = resident<E, D>(0);
+  plan.cluster = 1 << log2;
+  const long long waves = (units + slots - 1) / slots;
+  const long long alone = (log2 ? 1 : waves) * ((steps + plan.cluster - 1) / plan.cluster);
+  const long long shared = (units * steps + slots - 1) / slots + kJoinSteps;
+  if (alone > shared) plan.ctas = (int)(units * steps < slots ? units * steps : slots);
+}
 
 template <class E, int D>
 cudaError_t attn_e(const PagedAttnArgs& a, int gh, int* err, cudaStream_t s) {
@@ -765,24 +850,23 @@ cudaError_t attn_e(const PagedAttnArgs& a, int gh, int* err, cudaStream_t s) {
   const long long units = (long long)a.seqs * a.pool.heads * plan.chunks;
   long long most = (long long)a.width * a.pool.rows;  // positions of a unit
   if (a.window > 0 && a.window < most) most = a.window;
-  const long long steps = (most + E::kStep - 1) / E::kStep;
-  const int slots = resident_ctas<E, D>();
-  float* scratch = nullptr;
-  if (steps > kMinSteps && units < 8ll * slots) {
-    const long long worth = units * steps;
-    plan.ctas = (int)(worth < slots ? worth : slots);
-    const size_t parts = (size_t)plan.ctas * 2 * kHeadsMax;
-    const size_t bytes = parts * (D * sizeof(float) + sizeof(float2)) + plan.ctas * sizeof(int4);
-    const cudaError_t e = scratch_malloc((void**)&scratch, bytes, s);
-    if (e != cudaSuccess) return e;
-    plan.acc = scratch;
-    plan.ml = (float2*)(scratch + parts * D);
-    plan.meta = (int4*)(plan.ml + parts);
+  choose<E, D>(plan, units, (most + E::kStep - 1) / E::kStep);
+  if (plan.ctas == 0) {
+    launch_kernel_cluster(k_attn_paged<E, D>, (unsigned)(units * plan.cluster), kThreads, E::kSmem, s, plan.cluster, a, plan, err);
+    return cudaGetLastError();
   }
-  launch_kernel(k_attn_paged<E, D>, plan.ctas ? (unsigned)plan.ctas : (unsigned)units, kThreads, E::kSmem, s, a, plan, err);
-  if (!scratch) return cudaGetLastError();
+  float* scratch = nullptr;
+  const size_t parts = (size_t)plan.ctas * 2 * kHeadsMax;
+  const size_t bytes = parts * (D * sizeof(float) + sizeof(float2)) + plan.ctas * sizeof(int4);
+  cudaError_t e = scratch_malloc((void**)&scratch, bytes, s);
+  if (e != cudaSuccess) return e;
+  plan.acc = scratch;
+  plan.ml = (float2*)(scratch + parts * D);
+  plan.meta = (int4*)(plan.ml + parts);
+  launch_kernel(k_attn_paged<E, D>, (unsigned)plan.ctas, kThreads, E::kSmem, s, a, plan, err);
   launch_kernel(k_attn_join<typename E::T, D>, dim3(plan.ctas, group < gh ? group : gh), kJoinThreads, 0, s, a, plan);
-  const cudaError_t e = cudaGetLastError(), f = cudaFreeAsync(scratch, s);
+  e = cudaGetLastError();
+  const cudaError_t f = cudaFreeAsync(scratch, s);
   return e != cudaSuccess ? e : f;
 }
 
