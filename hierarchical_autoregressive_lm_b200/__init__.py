@@ -684,10 +684,31 @@ def attn_decode_scratch_bytes(dtype_code: int, G: int, H: int, head_dim: int, ca
     return int(out.value)
 
 
-def _rows(t, dtype, shape: tuple, name: str, out: bool = False) -> tuple:
-    """Host-side check of a strided tensor of rows (last dimension contiguous); its strides."""
-    import torch
-    if not isinstance(t, torch.Tensor):
+# ---- operators around a caller's paged KV cache ----
+# One decode step makes several of these calls, each a few microseconds on the
+# device, so the checks below take one short path and explain a refusal apart.
+
+_torch = None
+_raw_stream = None
+
+
+def _need_torch():
+    global _torch, _raw_stream
+    if _torch is None:
+        import torch
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+            lambda index: torch.cuda.current_stream(index).cuda_stream)
+        _torch = torch
+    return _torch
+
+
+def _rows(t, dtype, shape: tuple, dev: int, name: str, out: bool = False) -> tuple:
+    """Host-side check of a strided tensor of rows (last dimension contiguous) on device `dev`; its strides."""
+    if isinstance(t, _torch.Tensor) and t.dtype is dtype and t.shape == shape and t.get_device() == dev:
+        st = t.stride()
+        if (st[-1] == 1 or shape[-1] <= 1) and not (out and 0 in st):
+            return st
+    if not isinstance(t, _torch.Tensor):
         raise TypeError(f"{name}: expected a torch tensor, got {type(t).__name__}")
     if t.dtype != dtype:
         raise ValueError(f"{name}: expected {dtype}, got {t.dtype}")
@@ -696,39 +717,52 @@ def _rows(t, dtype, shape: tuple, name: str, out: bool = False) -> tuple:
     st = t.stride()
     if st[-1] != 1 and shape[-1] > 1:
         raise ValueError(f"{name}: the last dimension must be contiguous")
-    if out and 0 in st and any(s == 0 and n > 1 for s, n in zip(st, shape)):
+    if out and any(s == 0 and n > 1 for s, n in zip(st, shape)):
         raise ValueError(f"{name}: an output cannot be an expanded tensor")
-    if not t.is_cuda:
-        raise ValueError(f"{name}: must be a CUDA tensor")
+    _need_device(t, dev, name)
     return st
 
 
-def _launch(fn, tensors, stream, args) -> None:
-    """fn(*args, stream) on the device of the tensors, which must be one."""
-    import torch
-    dev = tensors[0].device
-    for t in tensors:
-        if t is not None and t.device != dev:
-            raise ValueError(f"tensors on {dev} and {t.device}")
-    if stream is None:
-        stream = torch.cuda.current_stream(dev)
-    s = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-    if dev.index == torch.cuda.current_device():
-        _check(fn(*args, s))
-    else:
-        with torch.cuda.device(dev):
-            _check(fn(*args, s))
+def _need_device(t, dev: int, name: str) -> None:
+    if not t.is_cuda:
+        raise ValueError(f"{name}: must be a CUDA tensor")
+    if t.get_device() != dev:
+        raise ValueError(f"{name}: on {t.device}, other tensors on cuda:{dev}")
+
+
+def _flat(t, dtype, numel: int, dev: int, name: str) -> int:
+    """Host-side check of a contiguous buffer of at least numel elements; its address."""
+    if not (isinstance(t, _torch.Tensor) and t.dtype is dtype and t.numel() >= numel and t.get_device() == dev
+            and t.is_contiguous()):
+        _need(t, dtype, numel, name)
+        _need_device(t, dev, name)
+    return t.data_ptr()
 
 
 def _code(t, name: str) -> int:
-    import torch
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name}: expected a torch tensor, got {type(t).__name__}")
-    if t.dtype == torch.bfloat16:
+    dtype = getattr(t, "dtype", None)
+    if dtype is _torch.bfloat16:
         return 1
-    if t.dtype == torch.float32:
+    if dtype is _torch.float32:
         return 0
-    raise ValueError(f"{name}: expected torch.float32 or torch.bfloat16, got {t.dtype}")
+    if not isinstance(t, _torch.Tensor):
+        raise TypeError(f"{name}: expected a torch tensor, got {type(t).__name__}")
+    raise ValueError(f"{name}: expected torch.float32 or torch.bfloat16, got {dtype}")
+
+
+def _launch(fn, dev: int, stream, args: tuple) -> None:
+    """fn(*args, stream) with device `dev` current."""
+    if stream is None:
+        s = _raw_stream(dev)
+    else:
+        s = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    if dev == _torch.cuda.current_device():
+        rc = fn(*args, s)
+    else:
+        with _torch.cuda.device(dev):
+            rc = fn(*args, s)
+    if rc:
+        _check(rc)
 
 
 class Rope:
@@ -742,21 +776,25 @@ class Rope:
     def __init__(self, rot_dim: int, theta: float = 10000.0, interleaved: bool = False, scaling: str = "none",
                  factor: float = 1.0, original_len: int = 0, alpha: float = 1.0, beta: float = 32.0,
                  attn_scale: float = 0.0, device="cuda"):
-        import torch
+        torch = _need_torch()
         if scaling not in self.SCALING:
             raise ValueError(f"scaling: expected one of {list(self.SCALING)}, got {scaling!r}")
         self.rot_dim, self.interleaved = int(rot_dim), bool(interleaved)
         cfg = photon_rope_config(self.rot_dim, self.SCALING[scaling], int(original_len), float(theta), float(factor),
                                  float(alpha), float(beta), float(attn_scale))
-        host = (ctypes.c_uint64 * max(1, self.rot_dim // 2))()
+        self._host = (ctypes.c_uint64 * max(1, self.rot_dim // 2))()
         scale = ctypes.c_float()
-        _check(load_library().photon_rope_frequencies(ctypes.byref(cfg), host, ctypes.byref(scale)))
-        self.turns, self.scale = list(host), float(scale.value)  # 2^64 * turns a position, on the host
-        self.freq = torch.tensor([x - (1 << 64) if x >> 63 else x for x in host], dtype=torch.int64).to(device)
-        if self.freq.is_cuda:
-            torch.cuda.current_stream(self.freq.device).synchronize()  # ready for every stream
+        _check(load_library().photon_rope_frequencies(ctypes.byref(cfg), self._host, ctypes.byref(scale)))
+        self.scale = float(scale.value)
+        # a copy from pageable memory has arrived when it returns: ready for every stream
+        self.freq = torch.frombuffer(self._host, dtype=torch.int64).to(device)
         self._t = photon_rope_table(self.freq.data_ptr(), self.rot_dim, int(self.interleaved), self.scale)
         self._ref = ctypes.addressof(self._t)
+
+    @property
+    def turns(self) -> list:
+        """2^64 * turns a position of each pair."""
+        return list(self._host)
 
 
 class KVPages:
@@ -766,30 +804,32 @@ class KVPages:
     float8_e4m3fn or int8 with k_scale, v_scale float32 [pages, heads, page_rows]."""
 
     def __init__(self, k, v, k_scale=None, v_scale=None):
-        import torch
+        torch = _need_torch()
         kinds = {torch.float32: 0, torch.bfloat16: 1, torch.float8_e4m3fn: 2, torch.int8: 3}
         for t, name in ((k, "k"), (v, "v")):
             if not isinstance(t, torch.Tensor):
                 raise TypeError(f"{name}: expected a torch tensor, got {type(t).__name__}")
             if t.dtype not in kinds or t.dim() != 4:
                 raise ValueError(f"{name}: expected [pages, heads, page_rows, head_dim] of {list(kinds)}")
-        kind = kinds[k.dtype]
+        kind, dev = kinds[k.dtype], k.get_device()
         if v.dtype != k.dtype or v.shape != k.shape:
             raise ValueError(f"v: expected {k.dtype} of shape {list(k.shape)}, as k")
         scales = (k_scale, v_scale)
         if (kind >= 2) != all(s is not None for s in scales) or (kind < 2 and any(s is not None for s in scales)):
             raise ValueError("k_scale and v_scale go with 8-bit pages, and only with them")
         shape = tuple(k.shape)
-        st = _rows(k, k.dtype, shape, "k", out=True)
-        if _rows(v, k.dtype, shape, "v", out=True) != st:
+        st = _rows(k, k.dtype, shape, dev, "k", out=True)
+        _need_device(k, dev, "k")
+        if _rows(v, k.dtype, shape, dev, "v", out=True) != st:
             raise ValueError("k and v must have the same strides")
         ss = (0, 0, 0)
         for s, name in zip(scales, ("k_scale", "v_scale")):
             if s is not None:
-                if s.dtype != torch.float32 or tuple(s.shape) != shape[:3] or not s.is_cuda:
+                if not isinstance(s, torch.Tensor) or s.dtype != torch.float32 or tuple(s.shape) != shape[:3]:
                     raise ValueError(f"{name}: expected CUDA torch.float32 {list(shape[:3])}")
                 if any(a == 0 and n > 1 for a, n in zip(s.stride(), shape)):
                     raise ValueError(f"{name}: an output cannot be an expanded tensor")
+                _need_device(s, dev, name)
         if kind >= 2:
             ss = k_scale.stride()
             if v_scale.stride() != ss:
@@ -797,9 +837,7 @@ class KVPages:
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
         self.pages, self.heads, self.page_rows, self.head_dim = shape
         self.dtype, self.device = k.dtype, k.device
-        if any(t is not None and t.device != self.device for t in (v, *scales)):
-            raise ValueError("k, v and their scales must be on one device")
-        self._wide = kind < 2
+        self._dev, self._wide, self._scale = dev, kind < 2, self.head_dim ** -0.5 if self.head_dim else 0.0
         self._p = photon_kv_pages(_ptr(k), _ptr(v), _ptr(k_scale), _ptr(v_scale), *st[:3], *ss, kind, *(
             self.pages, self.page_rows, self.heads, self.head_dim))
         self._ref = ctypes.addressof(self._p)
@@ -813,67 +851,71 @@ class KVPages:
             return cls(k, v)
         return cls(k, v, *(torch.zeros(pages, heads, page_rows, device=device) for _ in range(2)))
 
-    def _need(self, t, name: str) -> int:
+    def _code(self, t, name: str) -> int:
         code = _code(t, name)
-        if self._wide and t.dtype != self.dtype:
+        if self._wide and t.dtype is not self.dtype:
             raise ValueError(f"{name}: expected {self.dtype}, as the pages, got {t.dtype}")
         return code
 
 
 def _table(pages: KVPages, table) -> tuple:
-    import torch
+    """(pages, table, its row stride, sequences, width) as the entry points take them."""
     if not isinstance(pages, KVPages):
         raise TypeError(f"pages: expected KVPages, got {type(pages).__name__}")
-    if not isinstance(table, torch.Tensor) or table.dtype != torch.int32 or table.dim() != 2:
+    if not isinstance(table, _torch.Tensor) or table.dtype is not _torch.int32 or table.dim() != 2:
         raise ValueError("table: expected int32 [sequences, pages of each]")
     seqs, width = table.shape
-    if table.stride(1) != 1 and width > 1:
+    row, one = table.stride()
+    if one != 1 and width > 1:
         raise ValueError("table: the last dimension must be contiguous")
-    return seqs, width
+    if table.get_device() != pages._dev:
+        _need_device(table, pages._dev, "table")
+    return table.data_ptr(), row, seqs, width
 
 
 def rope(rope: Rope, pos, x, out, x2=None, out2=None, backward: bool = False, stream=None) -> None:
     """photon_rope: x, out [tokens, heads, head_dim] (any strides, last dimension contiguous)
     at positions pos (int32 [tokens]); x2, out2: a second tensor of the same tokens (q and
     k in one launch).  out may be x.  backward: the gradient of x from that of out."""
-    import torch
     if not isinstance(rope, Rope):
         raise TypeError(f"rope: expected Rope, got {type(rope).__name__}")
     code = _code(x, "x")
     if x.dim() != 3:
         raise ValueError("x: expected [tokens, heads, head_dim]")
-    n, heads, dim = x.shape
-    a, b = _rows(x, x.dtype, x.shape, "x"), _rows(out, x.dtype, x.shape, "out", out=True)
+    dtype, shape, dev = x.dtype, x.shape, x.get_device()
+    n, heads, dim = shape
+    if dev < 0 or rope.freq.get_device() != dev:
+        _need_device(x, dev, "x")
+        _need_device(rope.freq, dev, "rope")
+    a, b = _rows(x, dtype, shape, dev, "x"), _rows(out, dtype, shape, dev, "out", True)
+    p2 = o2 = None
     heads2, a2, b2 = 0, (0, 0), (0, 0)
     if x2 is not None:
-        if not isinstance(x2, torch.Tensor) or x2.dim() != 3:
+        if not isinstance(x2, _torch.Tensor) or x2.dim() != 3:
             raise ValueError("x2: expected [tokens, heads, head_dim]")
         heads2 = x2.shape[1]
-        a2, b2 = _rows(x2, x.dtype, (n, heads2, dim), "x2"), _rows(out2, x.dtype, (n, heads2, dim), "out2", out=True)
+        shape = (n, heads2, dim)
+        a2, b2 = _rows(x2, dtype, shape, dev, "x2"), _rows(out2, dtype, shape, dev, "out2", True)
+        p2, o2 = x2.data_ptr(), out2.data_ptr()
     elif out2 is not None:
         raise ValueError("out2 without x2")
-    _need(pos, torch.int32, n, "pos")
-    _launch(load_library().photon_rope, (x, out, x2, out2, pos, rope.freq), stream,
-            (code, rope._ref, pos.data_ptr(), n, dim, x.data_ptr(), a[0], a[1], heads, out.data_ptr(), b[0], b[1],
-             _ptr(x2), a2[0], a2[1], heads2, _ptr(out2), b2[0], b2[1], int(backward)))
+    _launch(load_library().photon_rope, dev, stream,
+            (code, rope._ref, _flat(pos, _torch.int32, n, dev, "pos"), n, dim, x.data_ptr(), a[0], a[1], heads,
+             out.data_ptr(), b[0], b[1], p2, a2[0], a2[1], heads2, o2, b2[0], b2[1], int(backward)))
 
 
 def _places(pages, table, pos, seq, k, v, out: bool, err) -> tuple:
-    import torch
-    seqs, width = _table(pages, table)
-    code = pages._need(k, "k")
-    n = pos.shape[0] if isinstance(pos, torch.Tensor) and pos.dim() == 1 else -1
-    if n < 0:
+    place = _table(pages, table)
+    code, dev = pages._code(k, "k"), pages._dev
+    if not isinstance(pos, _torch.Tensor) or pos.dim() != 1:
         raise ValueError("pos: expected int32 [tokens]")
+    n = pos.shape[0]
     shape = (n, pages.heads, pages.head_dim)
-    a, b = _rows(k, k.dtype, shape, "k", out), _rows(v, k.dtype, shape, "v", out)
-    _need(pos, torch.int32, n, "pos")
-    if seq is not None:
-        _need(seq, torch.int32, n, "seq")
-    if err is not None:
-        _need(err, torch.int32, 1, "err")
-    return (pages._ref, code, table.data_ptr(), table.stride(0), seqs, width, _ptr(seq), pos.data_ptr(), n,
-            k.data_ptr(), a[0], a[1], v.data_ptr(), b[0], b[1])
+    a, b = _rows(k, k.dtype, shape, dev, "k", out), _rows(v, k.dtype, shape, dev, "v", out)
+    i32 = _torch.int32
+    return (pages._ref, code, *place, None if seq is None else _flat(seq, i32, n, dev, "seq"),
+            _flat(pos, i32, n, dev, "pos"), n, k.data_ptr(), a[0], a[1], v.data_ptr(), b[0],
+            b[1]), None if err is None else _flat(err, i32, 1, dev, "err")
 
 
 def kv_write(pages: KVPages, table, pos, k, v, seq=None, rope: Rope = None, q=None, q_out=None, stream=None,
@@ -883,30 +925,35 @@ def kv_write(pages: KVPages, table, pos, k, v, seq=None, rope: Rope = None, q=No
     [sequences, pages of each]).  rope: rotates k on the way, and q [tokens, q_heads,
     head_dim] into q_out (may be q).  err: optional int32 CUDA tensor that receives a
     nonzero code when a place does not exist."""
-    args = _places(pages, table, pos, seq, k, v, False, err)
+    args, err = _places(pages, table, pos, seq, k, v, False, err)
+    dev, ref, qp, op = pages._dev, None, None, None
     heads, a, b = 0, (0, 0), (0, 0)
-    if rope is not None and not isinstance(rope, Rope):
-        raise TypeError(f"rope: expected Rope, got {type(rope).__name__}")
+    if rope is not None:
+        if not isinstance(rope, Rope):
+            raise TypeError(f"rope: expected Rope, got {type(rope).__name__}")
+        if rope.freq.get_device() != dev:
+            _need_device(rope.freq, dev, "rope")
+        ref = rope._ref
     if q is not None:
         if rope is None:
             raise ValueError("q is rotated, so it needs rope")
-        if q.dim() != 3:
+        if not isinstance(q, _torch.Tensor) or q.dim() != 3:
             raise ValueError("q: expected [tokens, heads, head_dim]")
         heads = q.shape[1]
         shape = (k.shape[0], heads, pages.head_dim)
-        a, b = _rows(q, k.dtype, shape, "q"), _rows(q_out, k.dtype, shape, "q_out", out=True)
+        a, b = _rows(q, k.dtype, shape, dev, "q"), _rows(q_out, k.dtype, shape, dev, "q_out", True)
+        qp, op = q.data_ptr(), q_out.data_ptr()
     elif q_out is not None:
         raise ValueError("q_out without q")
-    _launch(load_library().photon_kv_write,
-            (pages.k, table, pos, seq, k, v, q, q_out, None if rope is None else rope.freq, err), stream,
-            args + (None if rope is None else rope._ref, _ptr(q), a[0], a[1], heads, _ptr(q_out), b[0], b[1], _ptr(err)))
+    _launch(load_library().photon_kv_write, dev, stream,
+            (*args, ref, qp, a[0], a[1], heads, op, b[0], b[1], err))
 
 
 def kv_read(pages: KVPages, table, pos, k, v, seq=None, stream=None, err=None) -> None:
     """photon_kv_read: copies the places kv_write would write into k, v [tokens, heads,
     head_dim] (code * scale of an 8-bit cache); rows of padding tokens are left as they were."""
-    args = _places(pages, table, pos, seq, k, v, True, err)
-    _launch(load_library().photon_kv_read, (pages.k, table, pos, seq, k, v, err), stream, args + (_ptr(err),))
+    args, err = _places(pages, table, pos, seq, k, v, True, err)
+    _launch(load_library().photon_kv_read, pages._dev, stream, (*args, err))
 
 
 def attn_decode_paged(pages: KVPages, table, lens, q, out, window: int = 0, scale: Optional[float] = None, lse=None,
@@ -915,23 +962,19 @@ def attn_decode_paged(pages: KVPages, table, lens, q, out, window: int = 0, scal
     sequence, over the lens[b] (int32) positions of sequence b (the last `window` of them
     if given).  scale defaults to head_dim ** -0.5; lse: optional fp32 [sequences, q_heads]
     log-sum-exp of the scaled scores, for joining with attention over other keys."""
-    import torch
-    seqs, width = _table(pages, table)
-    code = pages._need(q, "q")
+    place = _table(pages, table)
+    code, dev = pages._code(q, "q"), pages._dev
     if q.dim() != 3:
         raise ValueError("q: expected [sequences, q_heads, head_dim]")
-    heads = q.shape[1]
+    seqs, heads = place[2], q.shape[1]
     shape = (seqs, heads, pages.head_dim)
-    a, b = _rows(q, q.dtype, shape, "q"), _rows(out, q.dtype, shape, "out", out=True)
-    _need(lens, torch.int32, seqs, "lens")
-    if lse is not None:
-        _need(lse, torch.float32, seqs * heads, "lse")
-    if err is not None:
-        _need(err, torch.int32, 1, "err")
-    _launch(load_library().photon_attn_decode_paged, (pages.k, table, lens, q, out, lse, err), stream,
-            (pages._ref, code, table.data_ptr(), table.stride(0), seqs, width, lens.data_ptr(), q.data_ptr(), a[0],
-             a[1], heads, int(window), pages.head_dim ** -0.5 if scale is None else float(scale), out.data_ptr(), b[0],
-             b[1], _ptr(lse), _ptr(err)))
+    a, b = _rows(q, q.dtype, shape, dev, "q"), _rows(out, q.dtype, shape, dev, "out", True)
+    i32 = _torch.int32
+    _launch(load_library().photon_attn_decode_paged, dev, stream,
+            (pages._ref, code, *place, _flat(lens, i32, seqs, dev, "lens"), q.data_ptr(), a[0], a[1], heads, int(window),
+             pages._scale if scale is None else float(scale), out.data_ptr(), b[0], b[1],
+             None if lse is None else _flat(lse, _torch.float32, seqs * heads, dev, "lse"),
+             None if err is None else _flat(err, i32, 1, dev, "err")))
 
 
 def debug_fail_alloc(n: int) -> None:
