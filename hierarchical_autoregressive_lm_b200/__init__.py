@@ -13,6 +13,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from typing import Optional
 
 __all__ = ["PhotonError", "Model", "Cache", "load_library", "LIB_PATH", "MODE_HIER",
@@ -124,6 +125,41 @@ class photon_kv_pages(ctypes.Structure):
                [(n, ctypes.c_int32) for n in ("kind", "pages", "page_rows", "heads", "head_dim")]
 
 
+# Arguments of the paged-cache operators: one structure of eight-byte fields a
+# call, packed by struct (a ctypes call costs a tenth of a microsecond for
+# every argument).
+class photon_rows(ctypes.Structure):
+    _fields_ = [("p", ctypes.c_void_p), ("token", ctypes.c_int64), ("head", ctypes.c_int64)]
+
+
+def _fields(names: str) -> list:
+    """"d_x:P n:q k:R ...": pointers, integers, rows, doubles."""
+    kinds = {"P": ctypes.c_void_p, "q": ctypes.c_int64, "R": photon_rows, "d": ctypes.c_double}
+    return [(n, kinds[k]) for n, k in (f.split(":") for f in names.split())]
+
+
+def _packer(cls) -> struct.Struct:
+    codes = {ctypes.c_void_p: "Q", ctypes.c_int64: "q", photon_rows: "Qqq", ctypes.c_double: "d"}
+    return struct.Struct("=" + "".join(codes[t] for _, t in cls._fields_))
+
+
+class photon_rope_args(ctypes.Structure):
+    _fields_ = _fields("rope:P d_pos:P dtype:q tokens:q head_dim:q backward:q x:R y:R heads:q x2:R y2:R heads2:q")
+
+
+class photon_kv_args(ctypes.Structure):
+    _fields_ = _fields("pages:P d_table:P table_stride:q seqs:q width:q d_seq:P d_pos:P dtype:q tokens:q k:R v:R "
+                       "d_err:P rope:P q:R q_out:R q_heads:q")
+
+
+class photon_attn_paged_args(ctypes.Structure):
+    _fields_ = _fields("pages:P d_table:P table_stride:q seqs:q width:q d_len:P dtype:q q_heads:q window:q q:R o:R "
+                       "d_lse:P d_err:P scale:d")
+
+
+_pack_rope, _pack_kv, _pack_attn = (_packer(c).pack for c in (photon_rope_args, photon_kv_args, photon_attn_paged_args))
+
+
 _lib: Optional[ctypes.CDLL] = None
 
 
@@ -177,12 +213,10 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         "photon_init_weights_levels": [ctypes.POINTER(photon_level_config), U64, ctypes.POINTER(P)],
         "photon_selftest_wait_timeout": [I64, P, P],
         "photon_rope_frequencies": [ctypes.POINTER(photon_rope_config), P, ctypes.POINTER(ctypes.c_float)],
-        "photon_rope": [I32, P, P, I32, I32, P, I64, I64, I32, P, I64, I64, P, I64, I64, I32, P, I64, I64, I32, P],
-        "photon_kv_write": [P, I32, P, I64, I32, I32, P, P, I32, P, I64, I64, P, I64, I64, P, P, I64, I64, I32, P,
-                            I64, I64, P, P],
-        "photon_kv_read": [P, I32, P, I64, I32, I32, P, P, I32, P, I64, I64, P, I64, I64, P, P],
-        "photon_attn_decode_paged": [P, I32, P, I64, I32, I32, P, P, I64, I64, I32, I32, ctypes.c_float, P, I64, I64,
-                                     P, P, P],
+        "photon_rope": [P, P],
+        "photon_kv_write": [P, P],
+        "photon_kv_read": [P, P],
+        "photon_attn_decode_paged": [P, P],
     }
     for name, args in sig.items():
         fn = getattr(L, name)
@@ -750,17 +784,17 @@ def _code(t, name: str) -> int:
     raise ValueError(f"{name}: expected torch.float32 or torch.bfloat16, got {dtype}")
 
 
-def _launch(fn, dev: int, stream, args: tuple) -> None:
-    """fn(*args, stream) with device `dev` current."""
+def _launch(fn, dev: int, stream, args: bytes) -> None:
+    """fn(args, stream) with device `dev` current."""
     if stream is None:
         s = _raw_stream(dev)
     else:
         s = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
     if dev == _torch.cuda.current_device():
-        rc = fn(*args, s)
+        rc = fn(args, s)
     else:
         with _torch.cuda.device(dev):
-            rc = fn(*args, s)
+            rc = fn(args, s)
     if rc:
         _check(rc)
 
@@ -888,8 +922,8 @@ def rope(rope: Rope, pos, x, out, x2=None, out2=None, backward: bool = False, st
         _need_device(x, dev, "x")
         _need_device(rope.freq, dev, "rope")
     a, b = _rows(x, dtype, shape, dev, "x"), _rows(out, dtype, shape, dev, "out", True)
-    p2 = o2 = None
-    heads2, a2, b2 = 0, (0, 0), (0, 0)
+    p2 = o2 = heads2 = 0
+    a2 = b2 = (0, 0)
     if x2 is not None:
         if not isinstance(x2, _torch.Tensor) or x2.dim() != 3:
             raise ValueError("x2: expected [tokens, heads, head_dim]")
@@ -900,8 +934,8 @@ def rope(rope: Rope, pos, x, out, x2=None, out2=None, backward: bool = False, st
     elif out2 is not None:
         raise ValueError("out2 without x2")
     _launch(load_library().photon_rope, dev, stream,
-            (code, rope._ref, _flat(pos, _torch.int32, n, dev, "pos"), n, dim, x.data_ptr(), a[0], a[1], heads,
-             out.data_ptr(), b[0], b[1], p2, a2[0], a2[1], heads2, o2, b2[0], b2[1], int(backward)))
+            _pack_rope(rope._ref, _flat(pos, _torch.int32, n, dev, "pos"), code, n, dim, int(backward), x.data_ptr(),
+                       a[0], a[1], out.data_ptr(), b[0], b[1], heads, p2, a2[0], a2[1], o2, b2[0], b2[1], heads2))
 
 
 def _places(pages, table, pos, seq, k, v, out: bool, err) -> tuple:
@@ -913,9 +947,9 @@ def _places(pages, table, pos, seq, k, v, out: bool, err) -> tuple:
     shape = (n, pages.heads, pages.head_dim)
     a, b = _rows(k, k.dtype, shape, dev, "k", out), _rows(v, k.dtype, shape, dev, "v", out)
     i32 = _torch.int32
-    return (pages._ref, code, *place, None if seq is None else _flat(seq, i32, n, dev, "seq"),
-            _flat(pos, i32, n, dev, "pos"), n, k.data_ptr(), a[0], a[1], v.data_ptr(), b[0],
-            b[1]), None if err is None else _flat(err, i32, 1, dev, "err")
+    return (pages._ref, *place, 0 if seq is None else _flat(seq, i32, n, dev, "seq"), _flat(pos, i32, n, dev, "pos"),
+            code, n, k.data_ptr(), a[0], a[1], v.data_ptr(), b[0], b[1],
+            0 if err is None else _flat(err, i32, 1, dev, "err"))
 
 
 def kv_write(pages: KVPages, table, pos, k, v, seq=None, rope: Rope = None, q=None, q_out=None, stream=None,
@@ -925,9 +959,9 @@ def kv_write(pages: KVPages, table, pos, k, v, seq=None, rope: Rope = None, q=No
     [sequences, pages of each]).  rope: rotates k on the way, and q [tokens, q_heads,
     head_dim] into q_out (may be q).  err: optional int32 CUDA tensor that receives a
     nonzero code when a place does not exist."""
-    args, err = _places(pages, table, pos, seq, k, v, False, err)
-    dev, ref, qp, op = pages._dev, None, None, None
-    heads, a, b = 0, (0, 0), (0, 0)
+    args = _places(pages, table, pos, seq, k, v, False, err)
+    dev, ref, qp, op, heads = pages._dev, 0, 0, 0, 0
+    a = b = (0, 0)
     if rope is not None:
         if not isinstance(rope, Rope):
             raise TypeError(f"rope: expected Rope, got {type(rope).__name__}")
@@ -946,14 +980,14 @@ def kv_write(pages: KVPages, table, pos, k, v, seq=None, rope: Rope = None, q=No
     elif q_out is not None:
         raise ValueError("q_out without q")
     _launch(load_library().photon_kv_write, dev, stream,
-            (*args, ref, qp, a[0], a[1], heads, op, b[0], b[1], err))
+            _pack_kv(*args, ref, qp, a[0], a[1], op, b[0], b[1], heads))
 
 
 def kv_read(pages: KVPages, table, pos, k, v, seq=None, stream=None, err=None) -> None:
     """photon_kv_read: copies the places kv_write would write into k, v [tokens, heads,
     head_dim] (code * scale of an 8-bit cache); rows of padding tokens are left as they were."""
-    args, err = _places(pages, table, pos, seq, k, v, True, err)
-    _launch(load_library().photon_kv_read, pages._dev, stream, (*args, err))
+    args = _places(pages, table, pos, seq, k, v, True, err)
+    _launch(load_library().photon_kv_read, pages._dev, stream, _pack_kv(*args, 0, 0, 0, 0, 0, 0, 0, 0))
 
 
 def attn_decode_paged(pages: KVPages, table, lens, q, out, window: int = 0, scale: Optional[float] = None, lse=None,
@@ -971,10 +1005,10 @@ def attn_decode_paged(pages: KVPages, table, lens, q, out, window: int = 0, scal
     a, b = _rows(q, q.dtype, shape, dev, "q"), _rows(out, q.dtype, shape, dev, "out", True)
     i32 = _torch.int32
     _launch(load_library().photon_attn_decode_paged, dev, stream,
-            (pages._ref, code, *place, _flat(lens, i32, seqs, dev, "lens"), q.data_ptr(), a[0], a[1], heads, int(window),
-             pages._scale if scale is None else float(scale), out.data_ptr(), b[0], b[1],
-             None if lse is None else _flat(lse, _torch.float32, seqs * heads, dev, "lse"),
-             None if err is None else _flat(err, i32, 1, dev, "err")))
+            _pack_attn(pages._ref, *place, _flat(lens, i32, seqs, dev, "lens"), code, heads, window, q.data_ptr(), a[0],
+                       a[1], out.data_ptr(), b[0], b[1],
+                       0 if lse is None else _flat(lse, _torch.float32, seqs * heads, dev, "lse"),
+                       0 if err is None else _flat(err, i32, 1, dev, "err"), pages._scale if scale is None else scale))
 
 
 def debug_fail_alloc(n: int) -> None:

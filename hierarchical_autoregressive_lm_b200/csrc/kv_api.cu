@@ -73,18 +73,31 @@ static int check_pool(const photon_kv_pages* p, int dtype, KvPoolArgs* out) {
   return PHOTON_OK;
 }
 
-static int check_table(const photon_kv_pages* p, const int32_t* table, int32_t seqs, int32_t width) {
-  if (seqs <= 0 || width <= 0) return refuse("table: empty shape [%d, %d]", seqs, width);
+static int check_table(const photon_kv_pages* p, const int32_t* table, int64_t seqs, int64_t width) {
+  if (seqs <= 0 || seqs > INT32_MAX || width <= 0) return refuse("table: shape [%lld, %lld]", (long long)seqs, (long long)width);
   if (!table || !aligned_to(table, 4)) return refuse("table: NULL or misaligned");
-  if ((int64_t)width * p->page_rows > (1 << 30)) return refuse("table: more than 2^30 positions a sequence");
+  if (width > (1 << 30) || width * p->page_rows > (1 << 30)) return refuse("table: more than 2^30 positions a sequence");
   return PHOTON_OK;
 }
 
-static int check_tokens(int32_t tokens, int64_t heads, const int32_t* pos, const int32_t* seq) {
+static int check_tokens(int64_t tokens, int64_t heads, const int32_t* pos, const int32_t* seq) {
   if (heads > (1 << 20)) return refuse("more than 2^20 heads");
   if (tokens < 0 || tokens > (1 << 30) || tokens * heads > INT32_MAX)
-    return refuse("tokens * heads must be below 2^31 (%d tokens)", tokens);
+    return refuse("tokens * heads must be below 2^31 (%lld tokens)", (long long)tokens);
   if (tokens > 0 && (!pos || !aligned_to(pos, 4) || !aligned_to(seq, 4))) return refuse("positions: NULL or misaligned");
+  return PHOTON_OK;
+}
+
+// Rows in, rows out.
+static HeadsArgs rows_of(const photon_rows* in, const photon_rows* out, int64_t heads) {
+  HeadsArgs h;
+  if (in) h.in = in->p, h.in_tok = in->token, h.in_head = in->head;
+  if (out) h.out = out->p, h.out_tok = out->token, h.out_head = out->head;
+  h.heads = (int)heads;
+  return h;
+}
+static int check_in_place(const photon_rows& x, const photon_rows& y) {
+  if (x.p == y.p && (x.token != y.token || x.head != y.head)) return refuse("in place needs equal strides");
   return PHOTON_OK;
 }
 
@@ -128,112 +141,112 @@ int photon_rope_frequencies(const photon_rope_config* c, uint64_t* h_freq, float
   return PHOTON_OK;
 }
 
-int photon_rope(int32_t dtype, const photon_rope_table* rope, const int32_t* d_pos, int32_t tokens, int32_t head_dim,
-                const void* d_x, int64_t x_token, int64_t x_head, int32_t heads, void* d_y, int64_t y_token,
-                int64_t y_head, const void* d_x2, int64_t x2_token, int64_t x2_head, int32_t heads2, void* d_y2,
-                int64_t y2_token, int64_t y2_head, int32_t backward, void* stream) {
+int photon_rope(const photon_rope_args* args, void* stream) {
   set_error_message("");
-  if (dtype != 0 && dtype != 1) return refuse("dtype must be 0 or 1");
-  if (!rope) return refuse("rope: NULL");
-  if (head_dim < 2 || head_dim > 512 || head_dim % 2) return refuse("head_dim %d must be even, 2..512", head_dim);
-  if (heads <= 0 || heads2 < 0) return refuse("heads: %d and %d", heads, heads2);
+  if (!args) return refuse("args: NULL");
+  const photon_rope_args& c = *args;
+  if (c.dtype != 0 && c.dtype != 1) return refuse("dtype must be 0 or 1");
+  if (!c.rope) return refuse("rope: NULL");
+  if (c.head_dim < 2 || c.head_dim > 512 || c.head_dim % 2) return refuse("head_dim must be even, 2..512");
+  if (c.heads <= 0 || c.heads2 < 0 || c.heads > (1 << 20) || c.heads2 > (1 << 20)) return refuse("heads out of range");
   RopeArgs r;
-  CHECK(check_rope(rope, head_dim, &r));
-  CHECK(check_tokens(tokens, (int64_t)heads + heads2, d_pos, nullptr));
-  if (tokens == 0) return PHOTON_OK;
-  CHECK(check_rows("x", dtype, d_x));
-  CHECK(check_rows("y", dtype, d_y));
-  HeadsArgs a, b;
-  a = {d_x, d_y, x_token, x_head, y_token, y_head, heads};
-  if (heads2) {
-    CHECK(check_rows("x2", dtype, d_x2));
-    CHECK(check_rows("y2", dtype, d_y2));
-    b = {d_x2, d_y2, x2_token, x2_head, y2_token, y2_head, heads2};
+  CHECK(check_rope(c.rope, (int)c.head_dim, &r));
+  CHECK(check_tokens(c.tokens, c.heads + c.heads2, c.d_pos, nullptr));
+  if (c.tokens == 0) return PHOTON_OK;
+  const int dt = (int)c.dtype;
+  CHECK(check_rows("x", dt, c.x.p));
+  CHECK(check_rows("y", dt, c.y.p));
+  CHECK(check_in_place(c.x, c.y));
+  HeadsArgs b;
+  if (c.heads2) {
+    CHECK(check_rows("x2", dt, c.x2.p));
+    CHECK(check_rows("y2", dt, c.y2.p));
+    CHECK(check_in_place(c.x2, c.y2));
+    b = rows_of(&c.x2, &c.y2, c.heads2);
   }
-  if ((d_x == d_y && (x_token != y_token || x_head != y_head)) ||
-      (heads2 && d_x2 == d_y2 && (x2_token != y2_token || x2_head != y2_head)))
-    return refuse("in place needs equal strides");
-  launch_rope(dtype, r, d_pos, tokens, head_dim, a, b, backward != 0, (cudaStream_t)stream);
+  launch_rope(dt, r, c.d_pos, (int)c.tokens, (int)c.head_dim, rows_of(&c.x, &c.y, c.heads), b, c.backward != 0,
+              (cudaStream_t)stream);
   return launched();
 }
 
-int photon_kv_write(const photon_kv_pages* pages, int32_t dtype, const int32_t* d_table, int64_t table_stride,
-                    int32_t seqs, int32_t width, const int32_t* d_seq, const int32_t* d_pos, int32_t tokens,
-                    const void* d_k, int64_t k_token, int64_t k_head, const void* d_v, int64_t v_token,
-                    int64_t v_head, const photon_rope_table* rope, const void* d_q, int64_t q_token, int64_t q_head,
-                    int32_t q_heads, void* d_q_out, int64_t qo_token, int64_t qo_head, int32_t* d_err, void* stream) {
+// What the write and the read check alike; *go: there is work to do.
+static int check_kv(const photon_kv_args* c, KvPoolArgs* p, KvPlaceArgs* pl, bool* go) {
+  *go = false;
+  if (!c) return refuse("args: NULL");
+  if (c->dtype != 0 && c->dtype != 1) return refuse("dtype must be 0 or 1");
+  CHECK(check_pool(c->pages, (int)c->dtype, p));
+  if (c->q_heads < 0 || c->q_heads > (1 << 20)) return refuse("q_heads out of range");
+  CHECK(check_tokens(c->tokens, p->heads + c->q_heads, c->d_pos, c->d_seq));
+  if (!aligned_to(c->d_err, 4)) return refuse("d_err: misaligned");
+  if (c->tokens == 0) return PHOTON_OK;
+  CHECK(check_table(c->pages, c->d_table, c->seqs, c->width));
+  CHECK(check_rows("k", (int)c->dtype, c->k.p));
+  CHECK(check_rows("v", (int)c->dtype, c->v.p));
+  *pl = {c->d_table, c->table_stride, (int)c->seqs, (int)c->width, c->d_seq, c->d_pos, (int)c->tokens};
+  *go = true;
+  return PHOTON_OK;
+}
+
+int photon_kv_write(const photon_kv_args* args, void* stream) {
   set_error_message("");
-  if (dtype != 0 && dtype != 1) return refuse("dtype must be 0 or 1");
   KvPoolArgs p;
-  CHECK(check_pool(pages, dtype, &p));
-  if (q_heads < 0) return refuse("q_heads: %d", q_heads);
-  CHECK(check_tokens(tokens, (int64_t)p.heads + q_heads, d_pos, d_seq));
+  KvPlaceArgs pl;
+  bool go;
+  CHECK(check_kv(args, &p, &pl, &go));
+  const photon_kv_args& c = *args;
   RopeArgs r;
-  if (rope) CHECK(check_rope(rope, p.dh, &r));
-  if (q_heads && !rope) return refuse("q is rotated, so it needs rope");
-  if (tokens == 0) return PHOTON_OK;
-  CHECK(check_table(pages, d_table, seqs, width));
-  CHECK(check_rows("k", dtype, d_k));
-  CHECK(check_rows("v", dtype, d_v));
-  const KvPlaceArgs pl = {d_table, table_stride, seqs, width, d_seq, d_pos, tokens};
-  HeadsArgs k, v, q;
-  k = {d_k, nullptr, k_token, k_head, 0, 0, p.heads};
-  v = {d_v, nullptr, v_token, v_head, 0, 0, p.heads};
-  if (q_heads) {
-    CHECK(check_rows("q", dtype, d_q));
-    CHECK(check_rows("q_out", dtype, d_q_out));
-    if (d_q == d_q_out && (q_token != qo_token || q_head != qo_head)) return refuse("in place needs equal strides");
-    q = {d_q, d_q_out, q_token, q_head, qo_token, qo_head, q_heads};
+  if (c.rope) CHECK(check_rope(c.rope, p.dh, &r));
+  if (c.q_heads && !c.rope) return refuse("q is rotated, so it needs rope");
+  if (!go) return PHOTON_OK;
+  const int dt = (int)c.dtype;
+  HeadsArgs q;
+  if (c.q_heads) {
+    CHECK(check_rows("q", dt, c.q.p));
+    CHECK(check_rows("q_out", dt, c.q_out.p));
+    CHECK(check_in_place(c.q, c.q_out));
+    q = rows_of(&c.q, &c.q_out, c.q_heads);
   }
-  launch_kv_write(dtype, p, pl, k, v, rope ? &r : nullptr, q, d_err, (cudaStream_t)stream);
+  launch_kv_write(dt, p, pl, rows_of(&c.k, nullptr, p.heads), rows_of(&c.v, nullptr, p.heads), c.rope ? &r : nullptr, q,
+                  c.d_err, (cudaStream_t)stream);
   return launched();
 }
 
-int photon_kv_read(const photon_kv_pages* pages, int32_t dtype, const int32_t* d_table, int64_t table_stride,
-                   int32_t seqs, int32_t width, const int32_t* d_seq, const int32_t* d_pos, int32_t tokens, void* d_k,
-                   int64_t k_token, int64_t k_head, void* d_v, int64_t v_token, int64_t v_head, int32_t* d_err,
-                   void* stream) {
+int photon_kv_read(const photon_kv_args* args, void* stream) {
   set_error_message("");
-  if (dtype != 0 && dtype != 1) return refuse("dtype must be 0 or 1");
   KvPoolArgs p;
-  CHECK(check_pool(pages, dtype, &p));
-  CHECK(check_tokens(tokens, p.heads, d_pos, d_seq));
-  if (tokens == 0) return PHOTON_OK;
-  CHECK(check_table(pages, d_table, seqs, width));
-  CHECK(check_rows("k", dtype, d_k));
-  CHECK(check_rows("v", dtype, d_v));
-  const KvPlaceArgs pl = {d_table, table_stride, seqs, width, d_seq, d_pos, tokens};
-  HeadsArgs k, v;
-  k = {nullptr, d_k, 0, 0, k_token, k_head, p.heads};
-  v = {nullptr, d_v, 0, 0, v_token, v_head, p.heads};
-  launch_kv_read(dtype, p, pl, k, v, d_err, (cudaStream_t)stream);
+  KvPlaceArgs pl;
+  bool go;
+  CHECK(check_kv(args, &p, &pl, &go));
+  if (args->rope || args->q_heads) return refuse("a read takes no rope and no q");
+  if (!go) return PHOTON_OK;
+  launch_kv_read((int)args->dtype, p, pl, rows_of(nullptr, &args->k, p.heads), rows_of(nullptr, &args->v, p.heads),
+                 args->d_err, (cudaStream_t)stream);
   return launched();
 }
 
-int photon_attn_decode_paged(const photon_kv_pages* pages, int32_t dtype, const int32_t* d_table,
-                             int64_t table_stride, int32_t seqs, int32_t width, const int32_t* d_len,
-                             const void* d_q, int64_t q_seq, int64_t q_head, int32_t q_heads, int32_t window,
-                             float scale, void* d_o, int64_t o_seq, int64_t o_head, float* d_lse, int32_t* d_err,
-                             void* stream) {
+int photon_attn_decode_paged(const photon_attn_paged_args* args, void* stream) {
   set_error_message("");
-  if (dtype != 0 && dtype != 1) return refuse("dtype must be 0 or 1");
+  if (!args) return refuse("args: NULL");
+  const photon_attn_paged_args& c = *args;
+  if (c.dtype != 0 && c.dtype != 1) return refuse("dtype must be 0 or 1");
   PagedAttnArgs a;
-  CHECK(check_pool(pages, dtype, &a.pool));
-  if (seqs == 0) return PHOTON_OK;
-  CHECK(check_table(pages, d_table, seqs, width));
-  if (q_heads <= 0 || q_heads % a.pool.heads) return refuse("q_heads %d must be a multiple of heads %d", q_heads, a.pool.heads);
-  if ((int64_t)seqs * q_heads > INT32_MAX) return refuse("seqs * q_heads must be below 2^31");
-  if (window < 0) return refuse("window: %d", window);
+  CHECK(check_pool(c.pages, (int)c.dtype, &a.pool));
+  if (c.seqs == 0) return PHOTON_OK;
+  CHECK(check_table(c.pages, c.d_table, c.seqs, c.width));
+  if (c.q_heads <= 0 || c.q_heads % a.pool.heads) return refuse("q_heads must be a multiple of heads %d", a.pool.heads);
+  if (c.q_heads > (1 << 20) || c.seqs * c.q_heads > INT32_MAX / 8) return refuse("seqs * q_heads must be below 2^28");
+  if (c.window < 0 || c.window > INT32_MAX) return refuse("window out of range");
+  const float scale = (float)c.scale;
   if (!std::isfinite(scale)) return refuse("scale must be finite");
-  if (!d_len || !aligned_to(d_len, 4)) return refuse("d_len: NULL or misaligned");
-  CHECK(check_rows("q", dtype, d_q));
-  CHECK(check_rows("o", dtype, d_o));
-  if (!aligned_to(d_lse, 4)) return refuse("d_lse: misaligned");
-  a.table = d_table, a.table_stride = table_stride, a.seqs = seqs, a.width = width, a.len = d_len;
-  a.q = d_q, a.q_seq = q_seq, a.q_head = q_head, a.q_heads = q_heads;
-  a.window = window, a.scale = scale;
-  a.o = d_o, a.o_seq = o_seq, a.o_head = o_head, a.lse = d_lse;
-  return result(launch_attn_paged(dtype, a, d_err, (cudaStream_t)stream));
+  if (!c.d_len || !aligned_to(c.d_len, 4)) return refuse("d_len: NULL or misaligned");
+  CHECK(check_rows("q", (int)c.dtype, c.q.p));
+  CHECK(check_rows("o", (int)c.dtype, c.o.p));
+  if (!aligned_to(c.d_lse, 4) || !aligned_to(c.d_err, 4)) return refuse("d_lse, d_err: misaligned");
+  a.table = c.d_table, a.table_stride = c.table_stride, a.seqs = (int)c.seqs, a.width = (int)c.width, a.len = c.d_len;
+  a.q = c.q.p, a.q_seq = c.q.token, a.q_head = c.q.head, a.q_heads = (int)c.q_heads;
+  a.window = (int)c.window, a.scale = scale;
+  a.o = c.o.p, a.o_seq = c.o.token, a.o_head = c.o.head, a.lse = c.d_lse;
+  return result(launch_attn_paged((int)c.dtype, a, c.d_err, (cudaStream_t)stream));
 }
 
 }  // extern "C"

@@ -631,9 +631,17 @@ PHOTON_API int photon_vanilla_free_cache(photon_vanilla_cache* c);
  * new token per sequence.  None of them has a counterpart in the PHOTON
  * paper.  All are asynchronous on `stream`, run on the current device (every
  * pointer must be accessible there), keep nothing between calls, and may be
- * captured into CUDA graphs.  dtype is the type of x, q, k, v and o: 0 fp32,
- * 1 bf16.  Strides count elements, the last dimension is contiguous, and a
- * stride may be anything that keeps distinct output elements apart. */
+ * captured into CUDA graphs.  Arguments come in one structure a call (fields
+ * of eight bytes; a caller packs them at once).  dtype is the type of x, q,
+ * k, v and o: 0 fp32, 1 bf16. */
+
+/* Rows [tokens][heads][head_dim] in device memory: row (t, h) starts at
+ * element t * token + h * head of p and is contiguous.  Strides may be
+ * anything that keeps distinct output elements apart. */
+typedef struct photon_rows {
+  void* p;
+  int64_t token, head; /* in elements */
+} photon_rows;
 
 /* Rotary positions.  Pair i (0 <= i < rot_dim/2) of a head turns by the
  * angle p * f_i at position p: (a, b) -> scale * (a cos - b sin, a sin + b
@@ -680,11 +688,16 @@ typedef struct photon_rope_table {
  * strides); otherwise the outputs overlap no input.  Angles are exact to
  * fp32 rounding, the arithmetic is fp32, the result is rounded once.
  * tokens = 0 is a no-op.  Errors: ERR_ARG, ERR_CUDA. */
-PHOTON_API int photon_rope(int32_t dtype, const photon_rope_table* rope, const int32_t* d_pos, int32_t tokens,
-                           int32_t head_dim, const void* d_x, int64_t x_token, int64_t x_head, int32_t heads,
-                           void* d_y, int64_t y_token, int64_t y_head, const void* d_x2, int64_t x2_token,
-                           int64_t x2_head, int32_t heads2, void* d_y2, int64_t y2_token, int64_t y2_head,
-                           int32_t backward, void* stream);
+typedef struct photon_rope_args {
+  const photon_rope_table* rope;
+  const int32_t* d_pos;
+  int64_t dtype, tokens, head_dim, backward;
+  photon_rows x, y;
+  int64_t heads;
+  photon_rows x2, y2; /* p = NULL and heads2 = 0: none */
+  int64_t heads2;
+} photon_rope_args;
+PHOTON_API int photon_rope(const photon_rope_args* args, void* stream);
 
 /* A pool of key and value pages of one layer, owned by the caller:
  * element (page, head, row, e) of K and of V sits at page * page_stride +
@@ -729,17 +742,21 @@ typedef struct photon_kv_pages {
  * product code * scale, rounded to dtype.  Rows of padding tokens are left as they were.  A
  * place may be named any number of times.
  * Errors: ERR_ARG, ERR_CUDA. */
-PHOTON_API int photon_kv_write(const photon_kv_pages* pages, int32_t dtype, const int32_t* d_table,
-                               int64_t table_stride, int32_t seqs, int32_t width, const int32_t* d_seq,
-                               const int32_t* d_pos, int32_t tokens, const void* d_k, int64_t k_token,
-                               int64_t k_head, const void* d_v, int64_t v_token, int64_t v_head,
-                               const photon_rope_table* rope, const void* d_q, int64_t q_token, int64_t q_head,
-                               int32_t q_heads, void* d_q_out, int64_t qo_token, int64_t qo_head,
-                               int32_t* d_err, void* stream);
-PHOTON_API int photon_kv_read(const photon_kv_pages* pages, int32_t dtype, const int32_t* d_table,
-                              int64_t table_stride, int32_t seqs, int32_t width, const int32_t* d_seq,
-                              const int32_t* d_pos, int32_t tokens, void* d_k, int64_t k_token, int64_t k_head,
-                              void* d_v, int64_t v_token, int64_t v_head, int32_t* d_err, void* stream);
+typedef struct photon_kv_args {
+  const photon_kv_pages* pages;
+  const int32_t* d_table; /* [seqs][width] */
+  int64_t table_stride, seqs, width;
+  const int32_t* d_seq; /* [tokens], nullable */
+  const int32_t* d_pos; /* [tokens] */
+  int64_t dtype, tokens;
+  photon_rows k, v;
+  int32_t* d_err;
+  const photon_rope_table* rope; /* from here on: of photon_kv_write, NULL and 0 for photon_kv_read */
+  photon_rows q, q_out;
+  int64_t q_heads;
+} photon_kv_args;
+PHOTON_API int photon_kv_write(const photon_kv_args* args, void* stream);
+PHOTON_API int photon_kv_read(const photon_kv_args* args, void* stream);
 
 /* Attention of one new token per sequence over its pages.  Sequence b holds
  * d_len[b] positions, the new token's own among them; query head h reads key
@@ -750,13 +767,21 @@ PHOTON_API int photon_kv_read(const photon_kv_pages* pages, int32_t dtype, const
  * A sequence without positions (length 0) gets o = 0 and lse = -infinity.
  * A length outside 0 .. width * page_rows is clamped to it and reported in
  * d_err, a page outside the pool leaves its positions out and is reported.
- * Softmax statistics and sums are fp32.  Allocates the scratch of its split
- * internally, as photon_attn_decode.  Errors: ERR_ARG, ERR_OOM, ERR_CUDA. */
-PHOTON_API int photon_attn_decode_paged(const photon_kv_pages* pages, int32_t dtype, const int32_t* d_table,
-                                        int64_t table_stride, int32_t seqs, int32_t width, const int32_t* d_len,
-                                        const void* d_q, int64_t q_seq, int64_t q_head, int32_t q_heads,
-                                        int32_t window, float scale, void* d_o, int64_t o_seq, int64_t o_head,
-                                        float* d_lse, int32_t* d_err, void* stream);
+ * Softmax statistics and sums are fp32.  A call that splits long contexts over
+ * the whole device takes its scratch from the library's stream-ordered pool
+ * and returns it on the stream, as photon_attn_decode.  Errors: ERR_ARG, ERR_OOM, ERR_CUDA. */
+typedef struct photon_attn_paged_args {
+  const photon_kv_pages* pages;
+  const int32_t* d_table; /* [seqs][width] */
+  int64_t table_stride, seqs, width;
+  const int32_t* d_len; /* [seqs] */
+  int64_t dtype, q_heads, window;
+  photon_rows q, o; /* a token per sequence */
+  float* d_lse;
+  int32_t* d_err;
+  double scale;
+} photon_attn_paged_args;
+PHOTON_API int photon_attn_decode_paged(const photon_attn_paged_args* args, void* stream);
 
 /* Number of kernels this library has launched in this process so far
  * (every launch of every entry point; host-side counter, no GPU access). */

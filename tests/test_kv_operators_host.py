@@ -81,12 +81,22 @@ BAD_PAGES = [dict(kind=4), dict(kind=-1), dict(kind=0), dict(pages=0), dict(page
              dict(row_stride=72), dict(head_stride=-8), dict(k_scale=A + 2)]
 
 
+def _call(fn, cls, defaults, kw):
+    """fn on a structure with the defaults changed by kw (rows: (address, token stride, head stride))."""
+    a = cls()
+    for n, v in {**defaults, **kw}.items():
+        if isinstance(v, ctypes.Structure):
+            v = ctypes.addressof(v)
+        setattr(a, n, hal.photon_rows(*v) if isinstance(v, tuple) else v)
+    return fn(ctypes.byref(a), None)
+
+
+ROWS, NONE = (A, 1024, 64), (None, 1024, 64)
+
+
 def _attn(lib, pages, **kw):
-    d = dict(dtype=1, table=A, stride=4, seqs=2, width=4, lens=A, q=A, q_heads=16, window=0, scale=0.125, o=A, lse=None)
-    d.update(kw)
-    return lib.photon_attn_decode_paged(None if pages is None else ctypes.byref(pages), d["dtype"], d["table"], d["stride"],
-                                        d["seqs"], d["width"], d["lens"], d["q"], 1024, 64, d["q_heads"], d["window"], d["scale"],
-                                        d["o"], 1024, 64, d["lse"], None, None)
+    d = dict(pages=pages, dtype=1, d_table=A, table_stride=4, seqs=2, width=4, d_len=A, q=ROWS, q_heads=16, window=0, scale=0.125, o=ROWS)
+    return _call(lib.photon_attn_decode_paged, hal.photon_attn_paged_args, d, kw)
 
 
 def test_attention_refusals():
@@ -94,68 +104,68 @@ def test_attention_refusals():
     for kw in BAD_PAGES:
         assert _attn(lib, _pages(**kw)) == -1, kw
         assert lib.photon_last_error() != b""
-    for kw in (dict(dtype=2), dict(table=None), dict(seqs=-1), dict(width=0), dict(width=1 << 28), dict(lens=None), dict(q=None), dict(o=None),
-               dict(q_heads=12), dict(q_heads=0), dict(window=-1), dict(scale=float("nan")), dict(scale=float("inf")),
-               dict(q=A + 1), dict(lse=A + 2), dict(table=A + 1), dict(seqs=1 << 28)):
+    for kw in (dict(dtype=2), dict(d_table=None), dict(seqs=-1), dict(width=0), dict(width=1 << 28), dict(width=1 << 40), dict(d_len=None),
+               dict(q=NONE), dict(o=NONE), dict(q_heads=12), dict(q_heads=0), dict(q_heads=1 << 40), dict(window=-1), dict(window=1 << 31),
+               dict(scale=float("nan")), dict(scale=float("inf")), dict(scale=1e39), dict(q=(A + 1, 1024, 64)), dict(d_lse=A + 2),
+               dict(d_err=A + 1), dict(d_table=A + 1), dict(seqs=1 << 28), dict(seqs=1 << 40)):
         assert _attn(lib, _pages(), **kw) == -1, kw
         assert lib.photon_last_error() != b""
     assert _attn(lib, None) == -1
-    assert _attn(lib, _pages(), seqs=0, table=None) == 0  # nothing to do
+    assert lib.photon_attn_decode_paged(None, None) == -1
+    assert _attn(lib, _pages(), seqs=0, d_table=None) == 0  # nothing to do
 
 
 def test_write_and_read_refusals():
     lib = hal.load_library()
     rope = hal.photon_rope_table(A, 64, 0, 1.0)
 
-    def write(pages, **kw):
-        d = dict(dtype=1, table=A, seqs=2, width=4, seq=None, pos=A, tokens=2, k=A, v=A, rope=None, q=None, q_heads=0, q_out=None, qs=1024)
-        d.update(kw)
-        return lib.photon_kv_write(ctypes.byref(pages), d["dtype"], d["table"], 4, d["seqs"], d["width"], d["seq"], d["pos"], d["tokens"],
-                                   d["k"], 512, 64, d["v"], 512, 64, None if d["rope"] is None else ctypes.byref(d["rope"]),
-                                   d["q"], d["qs"], 64, d["q_heads"], d["q_out"], 1024, 64, None, None)
-
-    def read(pages, **kw):
-        d = dict(dtype=1, table=A, seqs=2, width=4, seq=None, pos=A, tokens=2, k=A, v=A)
-        d.update(kw)
-        return lib.photon_kv_read(ctypes.byref(pages), d["dtype"], d["table"], 4, d["seqs"], d["width"], d["seq"], d["pos"], d["tokens"],
-                                  d["k"], 512, 64, d["v"], 512, 64, None, None)
-
-    for f in (write, read):
+    both = dict(dtype=1, d_table=A, table_stride=4, seqs=2, width=4, d_pos=A, tokens=2, k=ROWS, v=ROWS)
+    for fn in (lib.photon_kv_write, lib.photon_kv_read):
+        assert fn(None, None) == -1
         for kw in BAD_PAGES:
-            assert f(_pages(**kw)) == -1, kw
-        for kw in (dict(dtype=3), dict(table=None), dict(seqs=0), dict(width=-1), dict(pos=None), dict(tokens=-1), dict(k=None), dict(v=None),
-                   dict(tokens=1 << 29), dict(pos=A + 1), dict(seq=A + 2), dict(k=A + 1)):
-            assert f(_pages(), **kw) == -1, (f, kw)
+            assert _call(fn, hal.photon_kv_args, dict(both, pages=_pages(**kw)), {}) == -1, kw
+        pages = _pages()
+        for kw in (dict(pages=None), dict(dtype=3), dict(d_table=None), dict(seqs=0), dict(seqs=1 << 31), dict(width=-1), dict(d_pos=None),
+                   dict(tokens=-1), dict(k=NONE), dict(v=NONE), dict(tokens=1 << 29), dict(tokens=1 << 33), dict(d_pos=A + 1), dict(d_seq=A + 2),
+                   dict(d_err=A + 2), dict(k=(A + 1, 512, 64)), dict(q_heads=-1), dict(q_heads=1 << 33), dict(q=ROWS, q_out=ROWS, q_heads=16)):
+            assert _call(fn, hal.photon_kv_args, dict(both, pages=pages), kw) == -1, (fn, kw)
             assert lib.photon_last_error() != b""
-        assert f(_pages(), tokens=0, pos=None, k=None, v=None, table=None) == 0
+        assert _call(fn, hal.photon_kv_args, dict(both, pages=pages), dict(tokens=0, d_pos=None, k=NONE, v=NONE, d_table=None)) == 0
+    assert _call(lib.photon_kv_read, hal.photon_kv_args, dict(both, pages=pages), dict(rope=rope)) == -1
     for kw in (dict(rope=hal.photon_rope_table(None, 64, 0, 1.0)), dict(rope=hal.photon_rope_table(A, 66, 0, 1.0)),
-               dict(rope=hal.photon_rope_table(A, 31, 0, 1.0)), dict(q=A, q_out=A, q_heads=16), dict(rope=rope, q_heads=16, q=A),
-               dict(rope=rope, q_heads=16, q_out=A), dict(rope=rope, q_heads=-1), dict(rope=rope, q=A, q_out=A, q_heads=16, qs=2048)):
-        assert write(_pages(), **kw) == -1, kw
+               dict(rope=hal.photon_rope_table(A, 31, 0, 1.0)), dict(rope=rope, q_heads=16, q=ROWS),
+               dict(rope=rope, q_heads=16, q_out=ROWS), dict(rope=rope, q=ROWS, q_out=(A, 2048, 64), q_heads=16)):
+        assert _call(lib.photon_kv_write, hal.photon_kv_args, dict(both, pages=pages), kw) == -1, kw
 
 
 def test_rope_refusals():
     lib = hal.load_library()
     table = hal.photon_rope_table(A, 64, 0, 1.0)
-
-    def rope(t=table, **kw):
-        d = dict(dtype=0, pos=A, tokens=3, dim=64, x=A, heads=2, y=A, ys=128, x2=None, heads2=0, y2=None)
-        d.update(kw)
-        return lib.photon_rope(d["dtype"], None if t is None else ctypes.byref(t), d["pos"], d["tokens"], d["dim"], d["x"], 128, 64,
-                               d["heads"], d["y"], d["ys"], 64, d["x2"], 128, 64, d["heads2"], d["y2"], 128, 64, 0, None)
-
-    for kw in (dict(dtype=7), dict(pos=None), dict(tokens=-1), dict(dim=62), dict(dim=65), dict(dim=514), dict(x=None), dict(y=None),
-               dict(heads=0), dict(heads2=-1), dict(heads2=2), dict(heads2=2, x2=A), dict(ys=256), dict(x=A + 2), dict(tokens=1 << 30),
-               dict(t=None), dict(t=hal.photon_rope_table(A + 4, 64, 0, 1.0))):
-        assert rope(**kw) == -1, kw
+    rows = (A, 128, 64)
+    good = dict(rope=table, dtype=0, d_pos=A, tokens=3, head_dim=64, x=rows, heads=2, y=rows)
+    assert lib.photon_rope(None, None) == -1
+    for kw in (dict(dtype=7), dict(d_pos=None), dict(tokens=-1), dict(head_dim=62), dict(head_dim=65), dict(head_dim=514), dict(x=NONE),
+               dict(y=NONE), dict(heads=0), dict(heads=1 << 32), dict(heads2=-1), dict(heads2=2), dict(heads2=2, x2=rows), dict(y=(A, 256, 64)),
+               dict(heads2=1, x2=rows, y2=(A, 128, 32)), dict(x=(A + 2, 128, 64)), dict(tokens=1 << 30), dict(rope=None),
+               dict(rope=hal.photon_rope_table(A + 4, 64, 0, 1.0))):
+        assert _call(lib.photon_rope, hal.photon_rope_args, good, kw) == -1, kw
         assert lib.photon_last_error() != b""
-    assert rope(tokens=0, pos=None, x=None, y=None) == 0
+    assert _call(lib.photon_rope, hal.photon_rope_args, good, dict(tokens=0, d_pos=None, x=NONE, y=NONE)) == 0
 
 
 def test_struct_layouts():
     assert ctypes.sizeof(hal.photon_kv_pages) == 4 * 8 + 6 * 8 + 5 * 4 + 4
     assert ctypes.sizeof(hal.photon_rope_table) == 8 + 3 * 4 + 4
     assert ctypes.sizeof(hal.photon_rope_config) == 3 * 4 + 4 + 5 * 8
+    for cls, pack in ((hal.photon_rope_args, hal._pack_rope), (hal.photon_kv_args, hal._pack_kv), (hal.photon_attn_paged_args, hal._pack_attn)):
+        n = ctypes.sizeof(cls) // 8
+        packed = pack(*range(1, n + 1))
+        got, i = cls.from_buffer_copy(packed), 1
+        for name, kind in cls._fields_:
+            for value in ([getattr(got, name)] if kind is not hal.photon_rows else [getattr(getattr(got, name), f) for f in ("p", "token", "head")]):
+                assert value == i, (cls, name)
+                i += 1
+        assert i == n + 1
 
 
 def test_binding_refuses_before_the_library():
