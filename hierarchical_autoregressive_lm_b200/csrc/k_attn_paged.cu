@@ -39,7 +39,7 @@ constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 // How a launch deals out its work; parts are [cta][2][kHeadsMax].
 struct Plan {
-  int chunks, gh;  // units per key head, query heads of each
+  int chunks;      // units per key head
   int ctas;        // 0: a cluster per unit
   int cluster;
   int min_steps;   // least steps worth a CTA
@@ -67,50 +67,69 @@ __device__ __forceinline__ void ldsm_t(uint32_t (&r)[4], uint32_t a) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a));
 }
-// c[16 x 8] += a[16 x 16] b[16 x 8], fp32 accumulators.
-__device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                    uint32_t b1, bf16) {
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-               : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3]) : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+// c[16 x 8] += a[16 x 16] b[16 x 8] (tf32: a[16 x 8] b[8 x 8]), fp32 accumulators.
+#define PHOTON_MMA(shape, type)                                                                                    \
+  asm("mma.sync.aligned." shape ".row.col.f32." type "." type ".f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};" \
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3]) : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1))
+__device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+  PHOTON_MMA("m16n8k16", "bf16");
 }
-__device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                    uint32_t b1, __half) {
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-               : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3]) : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
+  PHOTON_MMA("m16n8k16", "f16");
+}
+__device__ __forceinline__ void mma_tf32(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+  PHOTON_MMA("m16n8k8", "tf32");
+}
+#undef PHOTON_MMA
+
+__device__ __forceinline__ float ld_shared(uint32_t a) {
+  float v;
+  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(a));
+  return v;
 }
 
-// Codes (four bytes) as fp16 pairs of bytes 0, 1 and 2, 3: exact.
+// 2^x to 2^-22 of itself, 0 below fp32's normal numbers.
+__device__ __forceinline__ float pow2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ float2 unpack_f16(uint32_t w) { return __half22float2(*reinterpret_cast<const __half2*>(&w)); }
+
+// Codes as fp16 pairs, exact: pairs of bytes 0, 1 and 2, 3, or (SKIP) 0, 2 and 1, 3.
+template <bool SKIP>
 __device__ __forceinline__ void codes_f16(uint32_t& lo, uint32_t& hi, uint32_t w, e4m3) {
+  if (SKIP) w = __byte_perm(w, 0, 0x3120);
   asm("{ .reg .b16 a, b; mov.b32 {a, b}, %2; cvt.rn.f16x2.e4m3x2 %0, a; cvt.rn.f16x2.e4m3x2 %1, b; }"
       : "=r"(lo), "=r"(hi) : "r"(w));
 }
+template <bool SKIP>
 __device__ __forceinline__ void codes_f16(uint32_t& lo, uint32_t& hi, uint32_t w, int8_t) {
   // code + 128 in the low bits of 1024
   w ^= 0x80808080u;
-  const uint32_t a = __byte_perm(w, 0x64646464u, 0x4140), b = __byte_perm(w, 0x64646464u, 0x4342);
+  const uint32_t a = __byte_perm(w, 0x64646464u, SKIP ? 0x4240 : 0x4140), b = __byte_perm(w, 0x64646464u, SKIP ? 0x4341 : 0x4342);
   const __half2 c = __floats2half2_rn(1152.f, 1152.f);
   const __half2 x = __hsub2(*reinterpret_cast<const __half2*>(&a), c), y = __hsub2(*reinterpret_cast<const __half2*>(&b), c);
   lo = *reinterpret_cast<const uint32_t*>(&x), hi = *reinterpret_cast<const uint32_t*>(&y);
 }
-// Codes as bf16 pairs of bytes 0, 2 and 1, 3: exact.
-__device__ __forceinline__ void codes_bf16(uint32_t& even, uint32_t& odd, uint32_t w, e4m3) {
-  uint32_t a, b;
-  codes_f16(a, b, __byte_perm(w, 0, 0x3120), e4m3{});
-  const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&a)), y = __half22float2(*reinterpret_cast<const __half2*>(&b));
-  even = pack_bf16(x.x, x.y), odd = pack_bf16(y.x, y.y);
-}
-__device__ __forceinline__ void codes_bf16(uint32_t& even, uint32_t& odd, uint32_t w, int8_t) {
-  // code + 128 in the low bits of 2^23
-  w ^= 0x80808080u;
-  float f[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) f[i] = __uint_as_float(__byte_perm(w, 0x4b000000u, 0x7440 + i)) - 8388736.f;
-  even = pack_bf16(f[0], f[2]), odd = pack_bf16(f[1], f[3]);
+
+// x as the sum of two tf32 numbers (the upper 19 bits of fp32), the first rounded, the second cut off.
+__device__ __forceinline__ void split_tf32(uint32_t& hi, uint32_t& lo, float x) {
+  hi = (__float_as_uint(x) + 0x1000u) & 0xffffe000u;
+  lo = __float_as_uint(x - __uint_as_float(hi)) & 0xffffe000u;
 }
 
 // What a unit's positions are.
 struct Unit {
-  int b, kh, h0, nh;  // sequence, key head, first query head and their number
+  int b, kh, h0, nh;  // sequence, key head, first query head and their number (at most kHeadsMax)
   int first, len;     // positions first .. len - 1
   const int* table;
 };
@@ -130,43 +149,24 @@ struct Joined {
   float m[kHeadsMax], l[kHeadsMax];
 };
 
-// bf16 queries on the tensor cores (m16n8k16: with eight query heads, one
-// token each, larger tiles would stay empty; the cache's bytes are the bound).
-//
-// A warp takes tiles of TP positions through a ring of cp.async stages of its
-// own, so no barrier stands between load and use; ldmatrix reads the rows,
-// whose 16-byte chunks are permuted so that eight rows fall into different
-// banks.  The heads are rows 0-7 of the products' left side; rows 8-15 carry
-// what rounding leaves behind, at no cost:
-//  * weights go to the second product as the sum of two bf16 numbers, off by
-//    2^-17 (one bf16 would be off by 2^-9, as much as the result's own rounding);
-//  * over 8-bit pages the first product runs in fp16, which holds every code
-//    exactly; q is divided by the power of two at its largest element and what
-//    fp16 cannot hold of it follows times 2^24.
-// In the second product the codes are bf16 (exact too): a weight times a
-// scale has fp32's range, which fp16 has not.
+// A warp's tiles of TP positions on their way through a ring of cp.async
+// stages of its own, so that no barrier stands between load and use.  The
+// 16-byte chunks of a row are permuted so that the rows that one instruction
+// reads fall into different banks.
 template <typename C, int D>
-struct TensorCores {
-  using T = bf16;
-  static constexpr int GH = kHeadsMax;
+struct Ring {
   static constexpr bool kNarrow = KvKind<C>::narrow;
   static constexpr int kRow = D * sizeof(C), kChunks = kRow / 16;
-  static constexpr int TP = 4096 / kRow < 16 ? 16 : 4096 / kRow > 64 ? 64 : 4096 / kRow;
-  static constexpr int kStep = kWarps * TP;
+  // 8 KB of keys and values a stage, where 16 to 64 positions make that
+  static constexpr int TP = kRow > 512 ? 8 : 4096 / kRow < 16 ? 16 : 4096 / kRow > 64 ? 64 : 4096 / kRow;
   static constexpr int kTile = TP * kRow;  // bytes of K (and of V)
-  static constexpr int kMeta = 16 + (kNarrow ? 8 * TP : 0);
-  static constexpr int kStage = 2 * kTile + kMeta;
+  static constexpr int kMeta = 16 + (kNarrow ? 8 * TP : 0);  // which positions exist, their scales
   static constexpr int kStages = 24576 / (2 * kTile) < 3 ? 3 : 24576 / (2 * kTile) > 6 ? 6 : 24576 / (2 * kTile);
-  static constexpr int kWarpBytes = kStages * kStage;
-  static constexpr int kSmem = kWarps * kWarpBytes;
-  static constexpr int kCtas = 2 * kSmem <= 220 * 1024 ? 2 : 1;
-  static_assert(kSmem >= (int)(sizeof(Joint<D>) + sizeof(Joined<D>)) && kTile % 128 == 0, "the ring is reused for the join");
-  static constexpr int KS = D / 16;   // k steps of the first product
-  static constexpr int NT = D / 8;    // column tiles of the second
-  static constexpr int SUB = TP / 16;
+  static constexpr int kBytes = kWarps * kStages * (2 * kTile + kMeta);
   static constexpr int PL = (TP + 31) / 32;  // positions a lane looks up
+  static_assert(kTile % 128 == 0, "tiles start at a bank line");
 
-  // Byte of chunk c of row r of a tile.
+  // Byte of chunk c of row r of a tile: eight rows' chunks c lie in different banks.
   static __device__ __forceinline__ uint32_t place(int r, int c) {
     if constexpr (kChunks >= 8) {
       return r * kRow + ((c ^ (r & 7)) << 4);
@@ -176,130 +176,220 @@ struct TensorCores {
       return line * 128 + ((((r % RPL) * kChunks + c) ^ (line & (kChunks - 1))) << 4);
     }
   }
+  // fp32 values are read by element, two neighbouring chunks of rows 0, 2, 4, 6 or 1, 3, 5, 7 at a time.
+  static __device__ __forceinline__ uint32_t place_v(int r, int c) {
+    if constexpr (sizeof(C) == 4)
+      return r * kRow + ((c ^ (r & 6)) << 4);
+    else
+      return place(r, c);
+  }
 
-  static __device__ __forceinline__ void run(const PagedAttnArgs& a, const Unit& u, int p0, int p1, unsigned char* smem,
-                                             int* err) {
+  const PagedAttnArgs& a;
+  const Unit& u;
+  int p0, p1, w, lane, mine;  // mine: tiles of this warp
+  uint32_t tiles;
+  unsigned char* metas;
+  int* err;
+
+  __device__ __forceinline__ Ring(const PagedAttnArgs& a_, const Unit& u_, int p0_, int p1_, unsigned char* smem, int* err_)
+      : a(a_), u(u_), p0(p0_), p1(p1_), w(threadIdx.x >> 5), lane(threadIdx.x & 31), err(err_) {
+    const int all = (p1 - p0 + TP - 1) / TP;
+    mine = all > w ? (all - w + kWarps - 1) / kWarps : 0;
+    tiles = ptx::smem_u32(smem) + w * (kStages * 2 * kTile);
+    metas = smem + kWarps * (kStages * 2 * kTile) + w * (kStages * kMeta);
+  }
+  __device__ __forceinline__ uint32_t keys(int i) const { return tiles + i % kStages * 2 * kTile; }
+  __device__ __forceinline__ const unsigned* exists(int i) const { return reinterpret_cast<const unsigned*>(metas + i % kStages * kMeta); }
+  __device__ __forceinline__ const float* scales(int i) const { return reinterpret_cast<const float*>(metas + i % kStages * kMeta + 16); }
+
+  // Pages of the warp's tile i.
+  __device__ __forceinline__ void look_up(int (&page)[PL], int i) const {
     const KvPoolArgs& p = a.pool;
-    const int w = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    const uint32_t ring = ptx::smem_u32(smem) + w * (kStages * 2 * kTile);
-    unsigned char* const metas = smem + kWarps * (kStages * 2 * kTile) + w * (kStages * kMeta);
-
-    // pages of this warp's tile i, and the copies of it
-    const int tiles = (p1 - p0 + TP - 1) / TP, mine = tiles > w ? (tiles - w + kWarps - 1) / kWarps : 0;
-    auto look_up = [&](int (&page)[PL], int i) {
+#pragma unroll
+    for (int j = 0; j < PL; ++j) {
+      const int pos = p0 + (w + i * kWarps) * TP + j * 32 + lane % TP;
+      page[j] = -1;
+      if (i < mine && pos < p1) {
+        page[j] = u.table[div_fast((uint32_t)pos, p.div)];
+        if ((uint32_t)page[j] >= (uint32_t)p.pages) report_error(err, DEV_BAD_PLACE), page[j] = -1;
+      }
+    }
+  }
+  // Starts its copies; rows that do not exist become zeros.
+  __device__ __forceinline__ void issue(const int (&page)[PL], int i) const {
+    const KvPoolArgs& p = a.pool;
+    if (i < mine) {
+      long long off[PL];
+      unsigned char* const meta = metas + i % kStages * kMeta;
 #pragma unroll
       for (int j = 0; j < PL; ++j) {
         const int pos = p0 + (w + i * kWarps) * TP + j * 32 + lane % TP;
-        page[j] = -1;
-        if (i < mine && pos < p1) {
-          page[j] = u.table[div_fast((uint32_t)pos, p.div)];
-          if ((uint32_t)page[j] >= (uint32_t)p.pages) report_error(err, DEV_BAD_PLACE), page[j] = -1;
+        const int row = pos - (int)div_fast((uint32_t)pos, p.div) * p.rows;
+        const bool ok = page[j] >= 0;
+        off[j] = ok ? page[j] * p.page + row * p.row + u.kh * p.head : -1;
+        const unsigned mask = __ballot_sync(0xffffffffu, ok);
+        if (lane == 0) reinterpret_cast<unsigned*>(meta)[j] = mask;
+        if (kNarrow && lane < TP) {
+          const long long s = ok ? page[j] * p.scale_page + row * p.scale_row + u.kh * p.scale_head : 0;
+          const uint32_t dst = ptx::smem_u32(meta + 16) + (j * 32 + lane) * 4;
+          cp4(dst, p.k_scale + s, ok);
+          cp4(dst + 4 * TP, p.v_scale + s, ok);
         }
       }
-    };
-    auto issue = [&](const int (&page)[PL], int i) {
-      if (i < mine) {
-        const int st = i % kStages;
-        long long off[PL];
-        unsigned char* const meta = metas + st * kMeta;
+      const uint32_t dst = keys(i);
 #pragma unroll
-        for (int j = 0; j < PL; ++j) {
-          const int pos = p0 + (w + i * kWarps) * TP + j * 32 + lane % TP;
-          const int row = pos - (int)div_fast((uint32_t)pos, p.div) * p.rows;
-          const bool ok = page[j] >= 0;
-          off[j] = ok ? page[j] * p.page + row * p.row + u.kh * p.head : -1;
-          const unsigned mask = __ballot_sync(0xffffffffu, ok);
-          if (lane == 0) reinterpret_cast<unsigned*>(meta)[j] = mask;
-          if (kNarrow && lane < TP) {
-            const long long s = ok ? page[j] * p.scale_page + row * p.scale_row + u.kh * p.scale_head : 0;
-            const uint32_t dst = ptx::smem_u32(meta + 16) + (j * 32 + lane) * 4;
-            cp4(dst, p.k_scale + s, ok);
-            cp4(dst + 4 * TP, p.v_scale + s, ok);
-          }
-        }
-        const uint32_t dst = ring + st * 2 * kTile;
-#pragma unroll
-        for (int n = 0; n < TP * kChunks / 32; ++n) {
-          const int id = n * 32 + lane, r = id / kChunks, c = id % kChunks;
-          // all lanes of one copy read rows of the same half of the tile
-          const long long o = __shfl_sync(0xffffffffu, off[n * 32 / kChunks / 32], r % 32);
-          const long long e = (o < 0 ? 0 : o) + c * (16 / (int)sizeof(C));
-          cp16(dst + place(r, c), (const C*)p.k + e, o >= 0);
-          cp16(dst + kTile + place(r, c), (const C*)p.v + e, o >= 0);
-        }
+      for (int n = 0; n < TP * kChunks / 32; ++n) {
+        const int id = n * 32 + lane, r = id / kChunks, c = id % kChunks;
+        // all lanes of one copy read rows of the same half of the tile
+        const long long o = __shfl_sync(0xffffffffu, off[n * 32 / kChunks / 32], r % 32);
+        const long long e = (o < 0 ? 0 : o) + c * (16 / (int)sizeof(C));
+        cp16(dst + place(r, c), (const C*)p.k + e, o >= 0);
+        cp16(dst + kTile + place_v(r, c), (const C*)p.v + e, o >= 0);
       }
-      cp_commit();
-    };
-
-    int page[PL];
-    {
-      int pages[kStages - 1][PL];
-#pragma unroll
-      for (int i = 0; i < kStages - 1; ++i) look_up(pages[i], i);
-#pragma unroll
-      for (int i = 0; i < kStages - 1; ++i) issue(pages[i], i);
-      look_up(page, kStages - 1);
     }
+    cp_commit();
+  }
+  // The first stages; `page` holds the pages of the tile after them.
+  __device__ __forceinline__ void start(int (&page)[PL]) const {
+    int pages[kStages - 1][PL];
+#pragma unroll
+    for (int i = 0; i < kStages - 1; ++i) look_up(pages[i], i);
+#pragma unroll
+    for (int i = 0; i < kStages - 1; ++i) issue(pages[i], i);
+    look_up(page, kStages - 1);
+  }
+  // Waits for tile i and starts the tile that takes the place of tile i - 1.
+  __device__ __forceinline__ void next(int (&page)[PL], int i) const {
+    cp_wait<kStages - 2>();
+    __syncwarp();  // every lane's copies of tile i are here, and tile i - 1 has been read
+    issue(page, i + kStages - 1);
+    look_up(page, i + kStages);
+  }
+};
 
-    // q: rows 0-7 of the left side, in the order of k that the codes come in
-    uint32_t qa[KS][kNarrow ? 4 : 2];
+// Positions of a tile that do not exist get no weight: s[n][e] is position 8 n + 2 t + e.
+template <int N>
+__device__ __forceinline__ void mask_scores(float (&s)[N][2], const unsigned* exists, int t) {
+#pragma unroll
+  for (int j = 0; j < (N + 3) / 4; ++j) {
+    const unsigned mask = exists[j];
+    if (mask != 0xffffffffu) {
+#pragma unroll
+      for (int n = 0; n < (N < 4 ? N : 4); ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          if (!((mask >> (8 * n + 2 * t + e)) & 1)) s[4 * j + n][e] = -INFINITY;
+    }
+  }
+}
+// The larger of m and a head's scores, which four lanes share.
+template <int N>
+__device__ __forceinline__ float largest_score(const float (&s)[N][2], float m) {
+  float x = -INFINITY;
+#pragma unroll
+  for (int n = 0; n < N; ++n) x = fmaxf(x, fmaxf(s[n][0], s[n][1]));
+  x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
+  x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
+  return fmaxf(x, m);
+}
+__device__ __forceinline__ float finite_base(float m) { return m == -INFINITY ? 0.f : m; }
+template <int N>
+__device__ __forceinline__ void scale_all(float (&o)[N][4], float f) {
+#pragma unroll
+  for (int n = 0; n < N; ++n)
+#pragma unroll
+    for (int k = 0; k < 4; ++k) o[n][k] *= f;
+}
+
+// Attention of a unit's query heads on the tensor cores.  With eight heads of
+// one token each, the warp-wide m16n8k16 wastes least; the cache's bytes are
+// the bound, not the products.  The heads are rows 0-7 of the products' left
+// side; rows 8-15 carry what rounding leaves behind, at no cost.
+//
+// bf16 pages: q, K and V are multiplied as they are; a weight goes in as the
+// sum of two bf16 numbers, off by 2^-17 (one would be off by 2^-9, as much as
+// the result's own rounding).
+//
+// 8-bit pages: both products run in fp16, which holds every code exactly.  q
+// is divided by the power of two at its largest element; what fp16 cannot
+// hold of it follows times 2^24, so q keeps 22 bits.  A weight times its
+// scale v has fp32's range, which fp16 has not: w = 2^(15 + s - z) |v|, with a
+// running maximum z of s + log2 |v| of its own, is at most 2^15, and what fp16
+// cannot hold of it follows times 2^11.  Weights keep 22 bits down to 2^-29
+// of the largest, and steps of 2^-50 of the largest below that.
+template <typename T_, typename C, int D>
+struct Half {
+  using T = T_;
+  using R = Ring<C, D>;
+  static constexpr bool kNarrow = KvKind<C>::narrow;
+  static constexpr int kStep = kWarps * R::TP;
+  static constexpr int kSmem = R::kBytes;
+  static constexpr int kCtas = 2 * kSmem <= 220 * 1024 ? 2 : 1;
+  static_assert(kSmem >= (int)(sizeof(Joint<D>) + sizeof(Joined<D>)), "the ring is reused for the join");
+  static constexpr int KS = D / 16;      // k steps of the first product
+  static constexpr int NT = D / 8;       // column tiles of the second
+  static constexpr int SUB = R::TP / 16;
+
+  // q: the left side, in the order of k that the keys come in.  Returns what turns products into log2 weights.
+  static __device__ __forceinline__ float load_q(uint32_t (&qa)[KS][kNarrow ? 4 : 2], const PagedAttnArgs& a, const Unit& u, int g, int t) {
+    const T* q = (const T*)a.q + u.b * a.q_seq + (u.h0 + g) * a.q_head;
+    const bool there = g < u.nh;
     float to_log2 = a.scale * kLog2e;
-    {
-      const T* q = (const T*)a.q + u.b * a.q_seq + (u.h0 + g) * a.q_head;
-      const bool there = g < u.nh;
-      if constexpr (kNarrow) {
-        float x[KS][4];
-        uint32_t top = 0;
+    if constexpr (kNarrow) {
+      float x[KS][4];
+      uint32_t top = 0;
 #pragma unroll
-        for (int k = 0; k < KS; ++k)
+      for (int k = 0; k < KS; ++k)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            x[k][i] = there ? ld_f(q + 16 * k + 4 * t + i) : 0.f;
-            top = max(top, __float_as_uint(x[k][i]) & 0x7fffffffu);
-          }
-        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        const uint32_t e = min(max(top >> 23, 1u), 253u);
-        to_log2 *= __uint_as_float(e << 23);
-        const float down = __uint_as_float((254 - e) << 23);
+        for (int i = 0; i < 4; ++i) {
+          x[k][i] = there ? ld_f(q + 16 * k + 4 * t + i) : 0.f;
+          top = max(top, __float_as_uint(x[k][i]) & 0x7fffffffu);
+        }
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      const uint32_t e = min(max(top >> 23, 1u), 253u);
+      to_log2 *= __uint_as_float(e << 23);
+      const float down = __uint_as_float((254 - e) << 23);
 #pragma unroll
-        for (int k = 0; k < KS; ++k)
+      for (int k = 0; k < KS; ++k)
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const float y = x[k][2 * i] * down, z = x[k][2 * i + 1] * down;
-            const __half2 h = __floats2half2_rn(y, z);
-            const float2 f = __half22float2(h);
-            const __half2 l = __floats2half2_rn(isfinite(y) ? (y - f.x) * 0x1p24f : 0.f, isfinite(z) ? (z - f.y) * 0x1p24f : 0.f);
-            qa[k][2 * i] = *reinterpret_cast<const uint32_t*>(&h);
-            qa[k][2 * i + 1] = *reinterpret_cast<const uint32_t*>(&l);
-          }
-      } else {
+        for (int i = 0; i < 2; ++i) {
+          const float y = x[k][2 * i] * down, z = x[k][2 * i + 1] * down;
+          const uint32_t h = pack_f16(y, z);
+          const float2 f = unpack_f16(h);
+          qa[k][2 * i] = h;
+          qa[k][2 * i + 1] = pack_f16(isfinite(y) ? (y - f.x) * 0x1p24f : 0.f, isfinite(z) ? (z - f.y) * 0x1p24f : 0.f);
+        }
+    } else {
 #pragma unroll
-        for (int k = 0; k < KS; ++k)
+      for (int k = 0; k < KS; ++k)
 #pragma unroll
-          for (int i = 0; i < 2; ++i)
-            qa[k][i] = there ? pack_bf16(ld_f(q + 16 * k + 8 * i + 2 * t), ld_f(q + 16 * k + 8 * i + 2 * t + 1)) : 0u;
-      }
+        for (int i = 0; i < 2; ++i)
+          qa[k][i] = there ? pack_bf16(ld_f(q + 16 * k + 8 * i + 2 * t), ld_f(q + 16 * k + 8 * i + 2 * t + 1)) : 0u;
     }
+    return to_log2;
+  }
 
-    float m = -INFINITY, l = 0.f, o[NT][4];
+  static __device__ __forceinline__ void run(const PagedAttnArgs& a, const Unit& u, int p0, int p1, unsigned char* smem,
+                                             int* err) {
+    const R ring(a, u, p0, p1, smem, err);
+    const int w = ring.w, lane = ring.lane, g = lane >> 2, t = lane & 3;
+    int page[R::PL];
+    ring.start(page);
+    uint32_t qa[KS][kNarrow ? 4 : 2];
+    const float to_log2 = load_q(qa, a, u, g, t);
+    float m = -INFINITY, z = -INFINITY, l = 0.f, o[NT][4];
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
       for (int i = 0; i < 4; ++i) o[n][i] = 0.f;
 
-    for (int i = 0; i < mine; ++i) {
-      cp_wait<kStages - 2>();
-      __syncwarp();  // every lane's copies of tile i are here, and tile i - 1 has been read
-      issue(page, i + kStages - 1);
-      look_up(page, i + kStages);
-      const int st = i % kStages;
-      const uint32_t kt = ring + st * 2 * kTile, vt = kt + kTile;
-      const unsigned char* const meta = metas + st * kMeta;
-      const float* const scales = reinterpret_cast<const float*>(meta + 16);
-
-      // scores: head g, positions 16 u + 8 j + 2 t + {0, 1}
-      float s[SUB][2][2];
+    for (int i = 0; i < ring.mine; ++i) {
+      ring.next(page, i);
+      const uint32_t kt = ring.keys(i), vt = kt + R::kTile;
+      const float* const scales = ring.scales(i);
+      // scores: head g, positions 8 n + 2 t + {0, 1}
+      float s[2 * SUB][2];
 #pragma unroll
       for (int u16 = 0; u16 < SUB; ++u16) {
         float c[2][4] = {};
@@ -307,93 +397,93 @@ struct TensorCores {
 #pragma unroll
         for (int k = 0; k < KS; k += kNarrow ? 2 : 1) {
           uint32_t x[4];
-          ldsm(x, kt + place(r, (kNarrow ? k : 2 * k) + ((lane >> 3) & 1)));
-          if constexpr (kNarrow) {
+          ldsm(x, kt + R::place(r, (kNarrow ? k : 2 * k) + ((lane >> 3) & 1)));
 #pragma unroll
-            for (int j = 0; j < 2; ++j)
+          for (int j = 0; j < 2; ++j) {
+            if constexpr (kNarrow) {
 #pragma unroll
               for (int kk = 0; kk < 2; ++kk) {
                 uint32_t b0, b1;
-                codes_f16(b0, b1, x[2 * j + kk], C());
-                mma(c[j], qa[k + kk][0], qa[k + kk][1], qa[k + kk][2], qa[k + kk][3], b0, b1, __half());
+                codes_f16<false>(b0, b1, x[2 * j + kk], C());
+                mma_f16(c[j], qa[k + kk][0], qa[k + kk][1], qa[k + kk][2], qa[k + kk][3], b0, b1);
               }
-          } else {
-#pragma unroll
-            for (int j = 0; j < 2; ++j) mma(c[j], qa[k][0], 0u, qa[k][1], 0u, x[2 * j], x[2 * j + 1], bf16());
+            } else {
+              mma_bf16(c[j], qa[k][0], 0u, qa[k][1], 0u, x[2 * j], x[2 * j + 1]);
+            }
           }
         }
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
+          const int n = 2 * u16 + j;
           if constexpr (kNarrow) {
-            const float2 ks = *reinterpret_cast<const float2*>(scales + u16 * 16 + j * 8 + 2 * t);
-            s[u16][j][0] = (c[j][0] + c[j][2] * 0x1p-24f) * to_log2 * ks.x;
-            s[u16][j][1] = (c[j][1] + c[j][3] * 0x1p-24f) * to_log2 * ks.y;
+            const float2 ks = *reinterpret_cast<const float2*>(scales + 8 * n + 2 * t);
+            s[n][0] = (c[j][0] + c[j][2] * 0x1p-24f) * to_log2 * ks.x;
+            s[n][1] = (c[j][1] + c[j][3] * 0x1p-24f) * to_log2 * ks.y;
           } else {
-            s[u16][j][0] = c[j][0] * to_log2;
-            s[u16][j][1] = c[j][1] * to_log2;
+            s[n][0] = c[j][0] * to_log2;
+            s[n][1] = c[j][1] * to_log2;
           }
         }
       }
+      mask_scores(s, ring.exists(i), t);
+
+      const float m_new = largest_score(s, m);
+      float base_w = finite_base(m_new);  // what the weights of the second product are relative to
+      if constexpr (kNarrow) {
+        float lv[2 * SUB][2];
 #pragma unroll
-      for (int j = 0; j < PL; ++j) {
-        const unsigned mask = reinterpret_cast<const unsigned*>(meta)[j];
-        if (mask != 0xffffffffu) {
-#pragma unroll
-          for (int n = 0; n < (SUB < 2 ? SUB : 2) * 4; ++n) {
-            const int at = n / 4 * 16 + (n / 2 % 2) * 8 + 2 * t + n % 2;
-            if (!((mask >> at) & 1)) s[j * 2 + n / 4][n / 2 % 2][n % 2] = -INFINITY;
-          }
+        for (int n = 0; n < 2 * SUB; ++n) {
+          const float2 vs = *reinterpret_cast<const float2*>(scales + R::TP + 8 * n + 2 * t);
+          // within +-120, so that neither 2^(s - z) nor its product with v leaves fp32
+          lv[n][0] = s[n][0] + fminf(fmaxf(__log2f(fabsf(vs.x)), -120.f), 120.f);
+          lv[n][1] = s[n][1] + fminf(fmaxf(__log2f(fabsf(vs.y)), -120.f), 120.f);
         }
+        const float z_new = largest_score(lv, z);
+        base_w = finite_base(z_new) - 15.f;
+        if (__any_sync(0xffffffffu, z_new != z)) scale_all(o, pow2(z - finite_base(z_new)));
+        z = z_new;
+      } else {
+        if (__any_sync(0xffffffffu, m_new != m)) scale_all(o, pow2(m - base_w));
       }
-      // softmax
-      float mx = -INFINITY;
-#pragma unroll
-      for (int n = 0; n < SUB * 4; ++n) mx = fmaxf(mx, s[n / 4][n / 2 % 2][n % 2]);
-      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-      mx = fmaxf(mx, m);
-      const float base = mx == -INFINITY ? 0.f : mx;
-      if (__any_sync(0xffffffffu, mx != m)) {
-        const float grow = exp2f(m - base);
-        l *= grow;
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-          for (int k = 0; k < 4; ++k) o[n][k] *= grow;
-      }
-      m = mx;
+      const float base = finite_base(m_new);
+      l *= pow2(m - base);
+      m = m_new;
 #pragma unroll
       for (int u16 = 0; u16 < SUB; ++u16) {
         uint32_t pa[4];
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          float x = exp2f(s[u16][j][0] - base), y = exp2f(s[u16][j][1] - base);
+          const int n = 2 * u16 + j;
+          float x = pow2(s[n][0] - base), y = pow2(s[n][1] - base);
           l += x + y;
           if constexpr (kNarrow) {
-            const float2 vs = *reinterpret_cast<const float2*>(scales + TP + u16 * 16 + j * 8 + 2 * t);
-            x *= vs.x, y *= vs.y;
+            const float2 vs = *reinterpret_cast<const float2*>(scales + R::TP + 8 * n + 2 * t);
+            x = pow2(s[n][0] - base_w) * vs.x, y = pow2(s[n][1] - base_w) * vs.y;
+            pa[2 * j] = pack_f16(x, y);
+            const float2 f = unpack_f16(pa[2 * j]);
+            pa[2 * j + 1] = pack_f16((x - f.x) * 0x1p11f, (y - f.y) * 0x1p11f);
+          } else {
+            const uint32_t hi = pack_bf16(x, y);
+            pa[2 * j] = hi;
+            pa[2 * j + 1] = pack_bf16(x - __uint_as_float(hi << 16), y - __uint_as_float(hi & 0xffff0000u));
           }
-          const uint32_t hi = pack_bf16(x, y);
-          pa[2 * j] = hi;
-          pa[2 * j + 1] = pack_bf16(x - __uint_as_float(hi << 16), y - __uint_as_float(hi & 0xffff0000u));
         }
         const int r = u16 * 16 + (lane & 15);
 #pragma unroll
-        for (int c = 0; c < kChunks; c += 2) {
+        for (int c = 0; c < R::kChunks; c += 2) {
           uint32_t x[4];
-          ldsm_t(x, vt + place(r, c + (lane >> 4)));
-          if constexpr (kNarrow) {
+          ldsm_t(x, vt + R::place(r, c + (lane >> 4)));
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
+          for (int j = 0; j < 2; ++j) {
+            if constexpr (kNarrow) {
               uint32_t e0, e1, o0, o1;
-              codes_bf16(e0, o0, x[2 * j], C());
-              codes_bf16(e1, o1, x[2 * j + 1], C());
-              mma(o[2 * (c + j)], pa[0], pa[1], pa[2], pa[3], e0, e1, bf16());
-              mma(o[2 * (c + j) + 1], pa[0], pa[1], pa[2], pa[3], o0, o1, bf16());
+              codes_f16<true>(e0, o0, x[2 * j], C());
+              codes_f16<true>(e1, o1, x[2 * j + 1], C());
+              mma_f16(o[2 * (c + j)], pa[0], pa[1], pa[2], pa[3], e0, e1);
+              mma_f16(o[2 * (c + j) + 1], pa[0], pa[1], pa[2], pa[3], o0, o1);
+            } else {
+              mma_bf16(o[c + j], pa[0], pa[1], pa[2], pa[3], x[2 * j], x[2 * j + 1]);
             }
-          } else {
-#pragma unroll
-            for (int j = 0; j < 2; ++j) mma(o[c + j], pa[0], pa[1], pa[2], pa[3], x[2 * j], x[2 * j + 1], bf16());
           }
         }
       }
@@ -406,10 +496,12 @@ struct TensorCores {
     float* const row = joint.o[w][g];
     if (t == 0) joint.m[w][g] = m, joint.l[w][g] = l;
     if constexpr (kNarrow) {
+      const float f = pow2(finite_base(z) - finite_base(m) - 15.f), f2 = f * 0x1p-11f;
 #pragma unroll
       for (int c = 0; c < NT / 2; ++c)
-        *reinterpret_cast<float4*>(row + 16 * c + 4 * t) = make_float4(o[2 * c][0] + o[2 * c][2], o[2 * c + 1][0] + o[2 * c + 1][2],
-                                                                       o[2 * c][1] + o[2 * c][3], o[2 * c + 1][1] + o[2 * c + 1][3]);
+        *reinterpret_cast<float4*>(row + 16 * c + 4 * t) =
+            make_float4(o[2 * c][0] * f + o[2 * c][2] * f2, o[2 * c + 1][0] * f + o[2 * c + 1][2] * f2,
+                        o[2 * c][1] * f + o[2 * c][3] * f2, o[2 * c + 1][1] * f + o[2 * c + 1][3] * f2);
     } else {
 #pragma unroll
       for (int n = 0; n < NT; ++n)
@@ -419,150 +511,101 @@ struct TensorCores {
   }
 };
 
-__device__ __forceinline__ float one_f(float x) { return x; }
-__device__ __forceinline__ float one_f(int8_t x) { return (float)x; }
-__device__ __forceinline__ float one_f(e4m3 x) {
-  return __half2float(__half(__nv_cvt_fp8_to_halfraw(x.x, __NV_E4M3)));
-}
-// N consecutive elements (at most 16 bytes a load) as fp32.
-template <int N, typename C>
-__device__ __forceinline__ void load_n(float (&v)[N], const C* p) {
-  constexpr int M = N * sizeof(C) > 16 ? 16 / (int)sizeof(C) : N;
-  struct alignas(M * sizeof(C)) Raw {
-    C x[M];
-  };
-#pragma unroll
-  for (int j = 0; j < N; j += M) {
-    const Raw r = *reinterpret_cast<const Raw*>(p + j);
-#pragma unroll
-    for (int i = 0; i < M; ++i) v[j + i] = one_f(r.x[i]);
-  }
-}
-
-// fp32 queries: everything in fp32, which the tensor cores do not multiply.
-// A warp takes tiles of 16 positions; lane (g, t) scores positions g and g +
-// 8 over every fourth group of eight elements, then sums D / 32 output
-// elements over the tile.
-template <typename C, int D, int GH_>
-struct CudaCores {
+// fp32 pages: q, K, V and the weights each as the sum of two tf32 numbers
+// (m16n8k8), 21 bits of them; the products of the two smaller parts come along.
+template <int D>
+struct Full {
   using T = float;
-  static constexpr int GH = GH_;
-  static constexpr int TP = 16, kStep = kWarps * TP;
-  static constexpr int VPL = D / 32;  // output elements of a lane
-  static constexpr int kCtas = 2;
-  struct Shared {
-    Joint<D> joint;
-    Joined<D> joined;
-    float q[GH][D];
-    float p[kWarps][TP][GH];
-    long long off[kWarps][TP];
-  };
-  static constexpr int kSmem = sizeof(Shared);
+  using R = Ring<float, D>;
+  static constexpr int kStep = kWarps * R::TP;
+  static constexpr int KS = D / 8, NT = D / 8, N8 = R::TP / 8;
+  static constexpr int kSmem = R::kBytes + KS * 32 * 16;  // the ring, and q
+  static constexpr int kCtas = 2 * kSmem <= 220 * 1024 ? 2 : 1;
+  static_assert(R::kBytes >= (int)(sizeof(Joint<D>) + sizeof(Joined<D>)), "the ring is reused for the join");
 
   static __device__ __forceinline__ void run(const PagedAttnArgs& a, const Unit& u, int p0, int p1, unsigned char* smem,
                                              int* err) {
-    Shared& sh = *reinterpret_cast<Shared*>(smem);
-    const KvPoolArgs& p = a.pool;
-    const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
-    for (int i = tid; i < GH * D; i += kThreads) {
-      const int h = i / D, e = i % D;
-      sh.q[h][e] = h < u.nh ? ((const T*)a.q)[u.b * a.q_seq + (u.h0 + h) * a.q_head + e] * (a.scale * kLog2e) : 0.f;
+    const R ring(a, u, p0, p1, smem, err);
+    const int w = ring.w, lane = ring.lane, g = lane >> 2, t = lane & 3;
+    uint4* const qs = reinterpret_cast<uint4*>(smem + R::kBytes);  // [k step][lane]
+    int page[R::PL];
+    ring.start(page);
+    {
+      const float* q = (const float*)a.q + u.b * a.q_seq + (u.h0 + g) * a.q_head;
+      for (int k = w; k < KS; k += kWarps) {
+        uint4 x;
+        split_tf32(x.x, x.y, g < u.nh ? q[8 * k + t] : 0.f);
+        split_tf32(x.z, x.w, g < u.nh ? q[8 * k + 4 + t] : 0.f);
+        qs[k * 32 + lane] = x;
+      }
     }
     __syncthreads();
-    float m[GH], l[GH], acc[GH][VPL];
+    const float to_log2 = a.scale * kLog2e;
+    float m = -INFINITY, l = 0.f, o[NT][4];
 #pragma unroll
-    for (int h = 0; h < GH; ++h) {
-      m[h] = -INFINITY, l[h] = 0.f;
+    for (int n = 0; n < NT; ++n)
 #pragma unroll
-      for (int i = 0; i < VPL; ++i) acc[h][i] = 0.f;
-    }
-    for (int t0 = p0 + w * TP; t0 < p1; t0 += kStep) {
-      // lanes 0..15 (and 16..31 again): place of one position, -1 where there is none
-      long long off = -1;
-      float ks = 1.f, vs = 1.f;
-      {
-        const int pos = t0 + lane % TP;
-        int page, row;
-        if (pos < p1 && page_of(u.table, a.width, p, pos, &page, &row, err)) {
-          off = page * p.page + row * p.row + u.kh * p.head;
-          if constexpr (KvKind<C>::narrow) {
-            const long long s = page * p.scale_page + row * p.scale_row + u.kh * p.scale_head;
-            ks = p.k_scale[s], vs = p.v_scale[s];
-          }
-        }
-        if (lane < TP) sh.off[w][lane] = off;
-      }
-      __syncwarp();
-      float s[2][GH];
+      for (int i = 0; i < 4; ++i) o[n][i] = 0.f;
+
+    for (int i = 0; i < ring.mine; ++i) {
+      ring.next(page, i);
+      const uint32_t kt = ring.keys(i), vt = kt + R::kTile;
+      float c[N8][4] = {};
 #pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        const long long o = sh.off[w][g + 8 * r];
+      for (int k = 0; k < KS; k += 2) {
+        const uint4 q0 = qs[k * 32 + lane], q1 = qs[k * 32 + 32 + lane];
 #pragma unroll
-        for (int h = 0; h < GH; ++h) s[r][h] = 0.f;
-        if (o >= 0) {
+        for (int n = 0; n < N8; ++n) {
+          uint32_t x[4], hi[4], lo[4];
+          ldsm(x, kt + R::place(8 * n + (lane & 7), 2 * k + (lane >> 3)));
 #pragma unroll
-          for (int i = 0; i < VPL; ++i) {
-            const int e = (t + 4 * i) * 8;
-            float x[8];
-            load8<true>(x, (const C*)p.k + o + e);
-#pragma unroll
-            for (int h = 0; h < GH; ++h) {
-              const float4 q0 = *reinterpret_cast<const float4*>(&sh.q[h][e]);
-              const float4 q1 = *reinterpret_cast<const float4*>(&sh.q[h][e + 4]);
-              s[r][h] += x[0] * q0.x + x[1] * q0.y + x[2] * q0.z + x[3] * q0.w + x[4] * q1.x + x[5] * q1.y +
-                         x[6] * q1.z + x[7] * q1.w;
-            }
-          }
+          for (int j = 0; j < 4; ++j) split_tf32(hi[j], lo[j], __uint_as_float(x[j]));
+          mma_tf32(c[n], q0.x, q0.y, q0.z, q0.w, hi[0], hi[1]);
+          mma_tf32(c[n], q0.x, q0.y, q0.z, q0.w, lo[0], lo[1]);
+          mma_tf32(c[n], q1.x, q1.y, q1.z, q1.w, hi[2], hi[3]);
+          mma_tf32(c[n], q1.x, q1.y, q1.z, q1.w, lo[2], lo[3]);
         }
       }
+      float s[N8][2];
 #pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        const bool seen = sh.off[w][g + 8 * r] >= 0;
-        const float k_scale = __shfl_sync(0xffffffffu, ks, g + 8 * r);
+      for (int n = 0; n < N8; ++n) s[n][0] = (c[n][0] + c[n][2]) * to_log2, s[n][1] = (c[n][1] + c[n][3]) * to_log2;
+      mask_scores(s, ring.exists(i), t);
+      const float m_new = largest_score(s, m), base = finite_base(m_new);
+      if (__any_sync(0xffffffffu, m_new != m)) {
+        const float grow = pow2(m - base);
+        l *= grow;
+        scale_all(o, grow);
+      }
+      m = m_new;
 #pragma unroll
-        for (int h = 0; h < GH; ++h) {
-          s[r][h] += __shfl_xor_sync(0xffffffffu, s[r][h], 1);
-          s[r][h] += __shfl_xor_sync(0xffffffffu, s[r][h], 2);
-          s[r][h] = seen ? s[r][h] * k_scale : -INFINITY;
+      for (int n = 0; n < N8; ++n) {
+        const float x = pow2(s[n][0] - base), y = pow2(s[n][1] - base);
+        l += x + y;
+        // k t of the product is position 2 t, k t + 4 is position 2 t + 1
+        uint32_t pa[4];
+        split_tf32(pa[0], pa[1], x);
+        split_tf32(pa[2], pa[3], y);
+        const int r = 8 * n + 2 * t;
+#pragma unroll
+        for (int d = 0; d < NT; ++d) {
+          const int chunk = 2 * d + (g >> 2);
+          uint32_t h0, h1, l0, l1;
+          split_tf32(h0, l0, ld_shared(vt + R::place_v(r, chunk) + (g & 3) * 4));
+          split_tf32(h1, l1, ld_shared(vt + R::place_v(r + 1, chunk) + (g & 3) * 4));
+          mma_tf32(o[d], pa[0], pa[1], pa[2], pa[3], h0, h1);
+          mma_tf32(o[d], pa[0], pa[1], pa[2], pa[3], l0, l1);
         }
       }
-      const float v0 = __shfl_sync(0xffffffffu, vs, g), v1 = __shfl_sync(0xffffffffu, vs, g + 8);
-#pragma unroll
-      for (int h = 0; h < GH; ++h) {
-        float mx = fmaxf(s[0][h], s[1][h]);
-#pragma unroll
-        for (int o = 4; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-        mx = fmaxf(mx, m[h]);
-        const float base = mx == -INFINITY ? 0.f : mx, grow = exp2f(m[h] - base);
-        const float x = exp2f(s[0][h] - base), y = exp2f(s[1][h] - base);
-        m[h] = mx;
-        l[h] = l[h] * grow + (x + y);
-#pragma unroll
-        for (int i = 0; i < VPL; ++i) acc[h][i] *= grow;
-        if (t == 0) sh.p[w][g][h] = x * v0, sh.p[w][g + 8][h] = y * v1;
-      }
-      __syncwarp();
-#pragma unroll 4
-      for (int j = 0; j < TP; ++j) {
-        const long long o = sh.off[w][j];
-        if (o < 0) continue;
-        float x[VPL];
-        load_n<VPL>(x, (const C*)p.v + o + lane * VPL);
-#pragma unroll
-        for (int h = 0; h < GH; ++h)
-#pragma unroll
-          for (int i = 0; i < VPL; ++i) acc[h][i] += sh.p[w][j][h] * x[i];
-      }
-      __syncwarp();
     }
+    cp_wait<0>();
+    l += __shfl_xor_sync(0xffffffffu, l, 1);
+    l += __shfl_xor_sync(0xffffffffu, l, 2);
+    __syncthreads();  // all rings have been read
+    Joint<D>& joint = *reinterpret_cast<Joint<D>*>(smem);
+    if (t == 0) joint.m[w][g] = m, joint.l[w][g] = l;
 #pragma unroll
-    for (int h = 0; h < GH; ++h) {
-#pragma unroll
-      for (int o = 4; o < 32; o <<= 1) l[h] += __shfl_xor_sync(0xffffffffu, l[h], o);
-      if (lane == 0) sh.joint.m[w][h] = m[h], sh.joint.l[w][h] = l[h];
-#pragma unroll
-      for (int i = 0; i < VPL; ++i) sh.joint.o[w][h][lane * VPL + i] = acc[h][i];
-    }
+    for (int n = 0; n < NT; ++n)
+      *reinterpret_cast<float2*>(joint.o[w][g] + 8 * n + 2 * t) = make_float2(o[n][0] + o[n][2], o[n][1] + o[n][3]);
     __syncthreads();
   }
 };
@@ -647,7 +690,7 @@ __device__ __forceinline__ Total total_of(int n, F&& get) {
 #pragma unroll
   for (int k = 0; k < N; ++k)
     if (k < n) {
-      const float f = exp2f(m[k] - base);
+      const float f = pow2(m[k] - base);
       t.l += f * l[k];
       t.o += f * o[k];
     }
@@ -690,10 +733,10 @@ __device__ __forceinline__ void put_cluster(const PagedAttnArgs& a, const Unit& 
 }
 
 __device__ __forceinline__ Unit unit_of(const PagedAttnArgs& a, const Plan& plan, int b, int unit, int* err) {
-  const int group = a.q_heads / a.pool.heads, skip = unit % plan.chunks * plan.gh;
+  const int group = a.q_heads / a.pool.heads, skip = unit % plan.chunks * kHeadsMax;
   Unit u;
   u.b = b, u.kh = unit / plan.chunks;
-  u.h0 = u.kh * group + skip, u.nh = min(plan.gh, group - skip);
+  u.h0 = u.kh * group + skip, u.nh = min(kHeadsMax, group - skip);
   u.len = length_of(a, b, err), u.first = first_of(a, u.len);
   u.table = a.table + b * a.table_stride;
   return u;
@@ -762,8 +805,8 @@ __global__ void __launch_bounds__(kJoinThreads) k_attn_join(const PagedAttnArgs 
   pdl_trigger();
   const int c = blockIdx.x, h = blockIdx.y, tid = threadIdx.x, group = a.q_heads / a.pool.heads;
   const int4 meta = plan.meta[c];
-  const int skip = meta.y % plan.chunks * plan.gh;
-  if (meta.z < 0 || h >= min(plan.gh, group - skip)) return;
+  const int skip = meta.y % plan.chunks * kHeadsMax;
+  if (meta.z < 0 || h >= min(kHeadsMax, group - skip)) return;
   const int parts = meta.z - c + 1;
   // the first part is slot 1 of CTA c, the others slot 0 of the CTAs after it
   auto slot = [&](int i) { return ((long long)(c + i) * 2 + (i == 0)) * kHeadsMax + h; };
@@ -782,7 +825,7 @@ __global__ void __launch_bounds__(kJoinThreads) k_attn_join(const PagedAttnArgs 
   for (int i = g; i < parts; i += G) {
     const float2 ml = plan.ml[slot(i)];
     const float4 x = reinterpret_cast<const float4*>(plan.acc + slot(i) * D)[e];
-    const float f = exp2f(ml.x - base);
+    const float f = pow2(ml.x - base);
     l += f * ml.y;
     o.x += f * x.x, o.y += f * x.y, o.z += f * x.z, o.w += f * x.w;
   }
@@ -842,10 +885,10 @@ void choose(Plan& plan, long long units, long long steps) {
 }
 
 template <class E, int D>
-cudaError_t attn_e(const PagedAttnArgs& a, int gh, int* err, cudaStream_t s) {
+cudaError_t attn_e(const PagedAttnArgs& a, int* err, cudaStream_t s) {
   const int group = a.q_heads / a.pool.heads;
   Plan plan = {};
-  plan.gh = gh, plan.chunks = (group + gh - 1) / gh;
+  plan.chunks = (group + kHeadsMax - 1) / kHeadsMax;
   plan.min_steps = kMinSteps;
   const long long units = (long long)a.seqs * a.pool.heads * plan.chunks;
   long long most = (long long)a.width * a.pool.rows;  // positions of a unit
@@ -864,7 +907,7 @@ cudaError_t attn_e(const PagedAttnArgs& a, int gh, int* err, cudaStream_t s) {
   plan.ml = (float2*)(scratch + parts * D);
   plan.meta = (int4*)(plan.ml + parts);
   launch_kernel(k_attn_paged<E, D>, (unsigned)plan.ctas, kThreads, E::kSmem, s, a, plan, err);
-  launch_kernel(k_attn_join<typename E::T, D>, dim3(plan.ctas, group < gh ? group : gh), kJoinThreads, 0, s, a, plan);
+  launch_kernel(k_attn_join<typename E::T, D>, dim3(plan.ctas, group < kHeadsMax ? group : kHeadsMax), kJoinThreads, 0, s, a, plan);
   e = cudaGetLastError();
   const cudaError_t f = cudaFreeAsync(scratch, s);
   return e != cudaSuccess ? e : f;
@@ -872,16 +915,13 @@ cudaError_t attn_e(const PagedAttnArgs& a, int gh, int* err, cudaStream_t s) {
 
 template <typename C, int D>
 cudaError_t attn_d(int dt, const PagedAttnArgs& a, int* err, cudaStream_t s) {
-  const int group = a.q_heads / a.pool.heads;
-  if constexpr (!std::is_same<C, float>::value)
-    if (dt == DT_BF16) return attn_e<TensorCores<C, D>, D>(a, kHeadsMax, err, s);
-  if constexpr (!std::is_same<C, bf16>::value) {
-    if (group <= 1) return attn_e<CudaCores<C, D, 1>, D>(a, 1, err, s);
-    if (group <= 2) return attn_e<CudaCores<C, D, 2>, D>(a, 2, err, s);
-    if (group <= 4) return attn_e<CudaCores<C, D, 4>, D>(a, 4, err, s);
-    return attn_e<CudaCores<C, D, 8>, D>(a, 8, err, s);
+  if constexpr (std::is_same<C, float>::value) {
+    return attn_e<Full<D>, D>(a, err, s);
+  } else {
+    if constexpr (KvKind<C>::narrow)
+      if (dt == DT_F32) return attn_e<Half<float, C, D>, D>(a, err, s);
+    return attn_e<Half<bf16, C, D>, D>(a, err, s);
   }
-  return cudaErrorInvalidValue;
 }
 
 template <typename C>

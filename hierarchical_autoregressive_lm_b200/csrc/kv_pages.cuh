@@ -29,31 +29,9 @@ template <> struct KvKind<int8_t> {
   static constexpr float top = 127.f;
 };
 
-// Eight consecutive elements as fp32.  VEC: the address is aligned to the
-// eight elements (16 bytes for fp32, which takes two loads).
-template <bool VEC>
-__device__ __forceinline__ void load8(float (&v)[8], const float* p) {
-  if constexpr (VEC) {
-    const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
-    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = p[i];
-  }
-}
 __device__ __forceinline__ void unpack_bf16(float* v, uint32_t w) {
   v[0] = __uint_as_float(w << 16);
   v[1] = __uint_as_float(w & 0xffff0000u);
-}
-template <bool VEC>
-__device__ __forceinline__ void load8(float (&v)[8], const bf16* p) {
-  if constexpr (VEC) {
-    const uint4 a = *reinterpret_cast<const uint4*>(p);
-    unpack_bf16(v, a.x), unpack_bf16(v + 2, a.y), unpack_bf16(v + 4, a.z), unpack_bf16(v + 6, a.w);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = __bfloat162float(p[i]);
-  }
 }
 __device__ __forceinline__ void unpack4(float* v, uint32_t w, e4m3) {
 #pragma unroll
@@ -67,17 +45,8 @@ __device__ __forceinline__ void unpack4(float* v, uint32_t w, int8_t) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) v[i] = (float)(int8_t)(w >> (8 * i));
 }
-template <bool VEC>
-__device__ __forceinline__ void load8(float (&v)[8], const e4m3* p) {
-  const uint2 a = *reinterpret_cast<const uint2*>(p);
-  unpack4(v, a.x, e4m3{}), unpack4(v + 4, a.y, e4m3{});
-}
-template <bool VEC>
-__device__ __forceinline__ void load8(float (&v)[8], const int8_t* p) {
-  const uint2 a = *reinterpret_cast<const uint2*>(p);
-  unpack4(v, a.x, int8_t{}), unpack4(v + 4, a.y, int8_t{});
-}
-
+// Eight consecutive elements from fp32.  VEC: the address is aligned to 16
+// bytes (8 for 8-bit elements).
 template <bool VEC>
 __device__ __forceinline__ void store8(float* p, const float (&v)[8]) {
   if constexpr (VEC) {
