@@ -85,6 +85,12 @@ __device__ __forceinline__ void mma_tf32(float (&c)[4], uint32_t a0, uint32_t a1
 }
 #undef PHOTON_MMA
 
+// An 8 x 8 matrix of 16-bit elements, two of row g in lane 4 g + t, transposed.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t y;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
 __device__ __forceinline__ float ld_shared(uint32_t a) {
   float v;
   asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(a));
@@ -160,9 +166,11 @@ struct Ring {
   // 8 KB of keys and values a stage, where 16 to 64 positions make that
   static constexpr int TP = kRow > 512 ? 8 : 4096 / kRow < 16 ? 16 : 4096 / kRow > 64 ? 64 : 4096 / kRow;
   static constexpr int kTile = TP * kRow;  // bytes of K (and of V)
-  static constexpr int kMeta = 16 + (kNarrow ? 8 * TP : 0);  // which positions exist, their scales
-  static constexpr int kStages = 24576 / (2 * kTile) < 3 ? 3 : 24576 / (2 * kTile) > 6 ? 6 : 24576 / (2 * kTile);
+  static constexpr int kMeta = 16 + (kNarrow ? 12 * TP : 0);  // which positions exist, their scales and log2 of V's
+  static constexpr int kRing = 16384;  // bytes of rows a warp has in flight or in use
+  static constexpr int kStages = kRing / (2 * kTile) < 2 ? 2 : kRing / (2 * kTile) > 6 ? 6 : kRing / (2 * kTile);
   static constexpr int kBytes = kWarps * kStages * (2 * kTile + kMeta);
+  static constexpr int kCtas = 3 * kBytes <= 222 * 1024 ? 3 : 2 * kBytes <= 222 * 1024 ? 2 : 1;
   static constexpr int PL = (TP + 31) / 32;  // positions a lane looks up
   static_assert(kTile % 128 == 0, "tiles start at a bank line");
 
@@ -190,6 +198,7 @@ struct Ring {
   uint32_t tiles;
   unsigned char* metas;
   int* err;
+  static constexpr uint32_t kNone = 0xffffffffu;
 
   __device__ __forceinline__ Ring(const PagedAttnArgs& a_, const Unit& u_, int p0_, int p1_, unsigned char* smem, int* err_)
       : a(a_), u(u_), p0(p0_), p1(p1_), w(threadIdx.x >> 5), lane(threadIdx.x & 31), err(err_) {
@@ -215,18 +224,19 @@ struct Ring {
       }
     }
   }
-  // Starts its copies; rows that do not exist become zeros.
+  // Starts its copies; rows that do not exist become zeros.  Rows are found by
+  // 32-bit offsets in the pool's units.
   __device__ __forceinline__ void issue(const int (&page)[PL], int i) const {
     const KvPoolArgs& p = a.pool;
     if (i < mine) {
-      long long off[PL];
+      uint32_t off[PL];
       unsigned char* const meta = metas + i % kStages * kMeta;
 #pragma unroll
       for (int j = 0; j < PL; ++j) {
         const int pos = p0 + (w + i * kWarps) * TP + j * 32 + lane % TP;
         const int row = pos - (int)div_fast((uint32_t)pos, p.div) * p.rows;
         const bool ok = page[j] >= 0;
-        off[j] = ok ? page[j] * p.page + row * p.row + u.kh * p.head : -1;
+        off[j] = ok ? (uint32_t)page[j] * p.page_u + (uint32_t)row * p.row_u + (uint32_t)u.kh * p.head_u : kNone;
         const unsigned mask = __ballot_sync(0xffffffffu, ok);
         if (lane == 0) reinterpret_cast<unsigned*>(meta)[j] = mask;
         if (kNarrow && lane < TP) {
@@ -241,10 +251,11 @@ struct Ring {
       for (int n = 0; n < TP * kChunks / 32; ++n) {
         const int id = n * 32 + lane, r = id / kChunks, c = id % kChunks;
         // all lanes of one copy read rows of the same half of the tile
-        const long long o = __shfl_sync(0xffffffffu, off[n * 32 / kChunks / 32], r % 32);
-        const long long e = (o < 0 ? 0 : o) + c * (16 / (int)sizeof(C));
-        cp16(dst + place(r, c), (const C*)p.k + e, o >= 0);
-        cp16(dst + kTile + place_v(r, c), (const C*)p.v + e, o >= 0);
+        const uint32_t o = __shfl_sync(0xffffffffu, off[n * 32 / kChunks / 32], r % 32);
+        const bool ok = o != kNone;
+        const unsigned long long at = (unsigned long long)(ok ? o : 0u) * p.unit + 16 * c;
+        cp16(dst + place(r, c), (const char*)p.k + at, ok);
+        cp16(dst + kTile + place_v(r, c), (const char*)p.v + at, ok);
       }
     }
     cp_commit();
@@ -301,10 +312,13 @@ __device__ __forceinline__ void scale_all(float (&o)[N][4], float f) {
     for (int k = 0; k < 4; ++k) o[n][k] *= f;
 }
 
-// Attention of a unit's query heads on the tensor cores.  With eight heads of
-// one token each, the warp-wide m16n8k16 wastes least; the cache's bytes are
-// the bound, not the products.  The heads are rows 0-7 of the products' left
-// side; rows 8-15 carry what rounding leaves behind, at no cost.
+// Attention of a unit's query heads on the tensor cores (m16n8k16): positions
+// or elements of the rows are the products' 16, the heads their 8 columns, so
+// little is wasted on heads of one token each; the cache's bytes are the
+// bound, not the products.  The weights' columns become the second product's
+// right side by a transposition within the warp.  With up to four heads
+// (PACK) the other four columns carry what rounding leaves behind, at no
+// cost; else that takes products of its own.
 //
 // bf16 pages: q, K and V are multiplied as they are; a weight goes in as the
 // sum of two bf16 numbers, off by 2^-17 (one would be off by 2^-9, as much as
@@ -315,25 +329,42 @@ __device__ __forceinline__ void scale_all(float (&o)[N][4], float f) {
 // hold of it follows times 2^24, so q keeps 22 bits.  A weight times its
 // scale v has fp32's range, which fp16 has not: w = 2^(15 + s - z) |v|, with a
 // running maximum z of s + log2 |v| of its own, is at most 2^15, and what fp16
-// cannot hold of it follows times 2^11.  Weights keep 22 bits down to 2^-29
-// of the largest, and steps of 2^-50 of the largest below that.
-template <typename T_, typename C, int D>
+// cannot hold of it follows.  Weights keep 22 bits down to 2^-17 of the
+// largest, and steps of 2^-39 of the largest below that.
+template <typename T_, typename C, int D, bool PACK>
 struct Half {
   using T = T_;
   using R = Ring<C, D>;
   static constexpr bool kNarrow = KvKind<C>::narrow;
   static constexpr int kStep = kWarps * R::TP;
   static constexpr int kSmem = R::kBytes;
-  static constexpr int kCtas = 2 * kSmem <= 220 * 1024 ? 2 : 1;
+  static constexpr int kCtas = R::kCtas;
   static_assert(kSmem >= (int)(sizeof(Joint<D>) + sizeof(Joined<D>)), "the ring is reused for the join");
-  static constexpr int KS = D / 16;      // k steps of the first product
-  static constexpr int NT = D / 8;       // column tiles of the second
+  static constexpr int KS = D / 16;        // k steps of the first product, row tiles of the second
   static constexpr int SUB = R::TP / 16;
+  static constexpr int QP = kNarrow && !PACK ? 2 : 1;  // parts of q that take products of their own
 
-  // q: the left side, in the order of k that the keys come in.  Returns what turns products into log2 weights.
-  static __device__ __forceinline__ float load_q(uint32_t (&qa)[KS][kNarrow ? 4 : 2], const PagedAttnArgs& a, const Unit& u, int g, int t) {
-    const T* q = (const T*)a.q + u.b * a.q_seq + (u.h0 + g) * a.q_head;
-    const bool there = g < u.nh;
+  static __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    if constexpr (kNarrow)
+      mma_f16(c, a[0], a[1], a[2], a[3], b0, b1);
+    else
+      mma_bf16(c, a[0], a[1], a[2], a[3], b0, b1);
+  }
+  static __device__ __forceinline__ uint32_t pack(float x, float y) {
+    if constexpr (kNarrow) return pack_f16(x, y);
+    else return pack_bf16(x, y);
+  }
+  static __device__ __forceinline__ float2 unpack(uint32_t w) {
+    if constexpr (kNarrow) return unpack_f16(w);
+    else return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+  }
+
+  // q as the right side of the first product, in the order of k that the keys
+  // come in: column g.  Returns what turns its products into log2 weights.
+  static __device__ __forceinline__ float load_q(uint32_t (&qb)[KS][QP][2], const PagedAttnArgs& a, const Unit& u, int g, int t) {
+    const int head = PACK ? g & 3 : g;
+    const T* q = (const T*)a.q + u.b * a.q_seq + (u.h0 + head) * a.q_head;
+    const bool there = head < u.nh;
     float to_log2 = a.scale * kLog2e;
     if constexpr (kNarrow) {
       float x[KS][4];
@@ -357,17 +388,31 @@ struct Half {
           const float y = x[k][2 * i] * down, z = x[k][2 * i + 1] * down;
           const uint32_t h = pack_f16(y, z);
           const float2 f = unpack_f16(h);
-          qa[k][2 * i] = h;
-          qa[k][2 * i + 1] = pack_f16(isfinite(y) ? (y - f.x) * 0x1p24f : 0.f, isfinite(z) ? (z - f.y) * 0x1p24f : 0.f);
+          const uint32_t l = pack_f16(isfinite(y) ? (y - f.x) * 0x1p24f : 0.f, isfinite(z) ? (z - f.y) * 0x1p24f : 0.f);
+          qb[k][0][i] = PACK && g >= 4 ? l : h;
+          if constexpr (QP == 2) qb[k][1][i] = l;
         }
     } else {
 #pragma unroll
       for (int k = 0; k < KS; ++k)
 #pragma unroll
         for (int i = 0; i < 2; ++i)
-          qa[k][i] = there ? pack_bf16(ld_f(q + 16 * k + 8 * i + 2 * t), ld_f(q + 16 * k + 8 * i + 2 * t + 1)) : 0u;
+          qb[k][0][i] = there ? pack_bf16(ld_f(q + 16 * k + 8 * i + 2 * t), ld_f(q + 16 * k + 8 * i + 2 * t + 1)) : 0u;
     }
     return to_log2;
+  }
+
+  // Largest over a column pair's positions, which eight lanes share, and x.
+  static __device__ __forceinline__ void largest_of(float (&m)[2], const float (&s)[2 * SUB][2], const float (&x)[2]) {
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      float y = s[0][e];
+#pragma unroll
+      for (int n = 1; n < 2 * SUB; ++n) y = fmaxf(y, s[n][e]);
+#pragma unroll
+      for (int o = 4; o < 32; o <<= 1) y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, o));
+      m[e] = fmaxf(x[e], y);
+    }
   }
 
   static __device__ __forceinline__ void run(const PagedAttnArgs& a, const Unit& u, int p0, int p1, unsigned char* smem,
@@ -376,11 +421,17 @@ struct Half {
     const int w = ring.w, lane = ring.lane, g = lane >> 2, t = lane & 3;
     int page[R::PL];
     ring.start(page);
-    uint32_t qa[KS][kNarrow ? 4 : 2];
-    const float to_log2 = load_q(qa, a, u, g, t);
-    float m = -INFINITY, z = -INFINITY, l = 0.f, o[NT][4];
+    uint32_t qb[KS][QP][2];
+    float to_log2[2];  // of columns 2 t, 2 t + 1
+    {
+      const float f = load_q(qb, a, u, g, t);
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
+      for (int e = 0; e < 2; ++e) to_log2[e] = __shfl_sync(0xffffffffu, f, (2 * t + e) * 4);
+    }
+    // columns 2 t, 2 t + 1: maxima of s and of s + log2 |v|, sums; rows g, g + 8 of the row tiles
+    float m[2] = {-INFINITY, -INFINITY}, z[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, o[KS][4];
+#pragma unroll
+    for (int n = 0; n < KS; ++n)
 #pragma unroll
       for (int i = 0; i < 4; ++i) o[n][i] = 0.f;
 
@@ -388,124 +439,165 @@ struct Half {
       ring.next(page, i);
       const uint32_t kt = ring.keys(i), vt = kt + R::kTile;
       const float* const scales = ring.scales(i);
-      // scores: head g, positions 8 n + 2 t + {0, 1}
+      if constexpr (kNarrow) {
+        // log2 |v| of every position, within +-120, so that neither 2^(s - z) nor its product with v leaves fp32
+#pragma unroll
+        for (int j = 0; j < R::PL; ++j)
+          if (j * 32 + lane < R::TP) {
+            const float lv = __log2f(fabsf(scales[R::TP + j * 32 + lane]));
+            const_cast<float*>(scales)[2 * R::TP + j * 32 + lane] = fminf(fmaxf(lv, -120.f), 120.f);
+          }
+        __syncwarp();
+      }
+      // scores s[n]: position 8 n + g
       float s[2 * SUB][2];
 #pragma unroll
       for (int u16 = 0; u16 < SUB; ++u16) {
-        float c[2][4] = {};
-        const int r = u16 * 16 + (lane & 7) + (lane >> 4) * 8;
+        float c[QP][4] = {};
+        const int r = u16 * 16 + (lane & 15);
+        if constexpr (kNarrow) {
 #pragma unroll
-        for (int k = 0; k < KS; k += kNarrow ? 2 : 1) {
-          uint32_t x[4];
-          ldsm(x, kt + R::place(r, (kNarrow ? k : 2 * k) + ((lane >> 3) & 1)));
+          for (int k = 0; k < KS; k += 2) {
+            uint32_t x[4];
+            ldsm(x, kt + R::place(r, k + (lane >> 4)));
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            if constexpr (kNarrow) {
+            for (int kk = 0; kk < 2; ++kk) {
+              uint32_t f[4];
+              codes_f16<false>(f[0], f[2], x[2 * kk], C());
+              codes_f16<false>(f[1], f[3], x[2 * kk + 1], C());
 #pragma unroll
-              for (int kk = 0; kk < 2; ++kk) {
-                uint32_t b0, b1;
-                codes_f16<false>(b0, b1, x[2 * j + kk], C());
-                mma_f16(c[j], qa[k + kk][0], qa[k + kk][1], qa[k + kk][2], qa[k + kk][3], b0, b1);
-              }
-            } else {
-              mma_bf16(c[j], qa[k][0], 0u, qa[k][1], 0u, x[2 * j], x[2 * j + 1]);
+              for (int j = 0; j < QP; ++j) mma(c[j], f, qb[k + kk][j][0], qb[k + kk][j][1]);
             }
           }
+        } else {
+#pragma unroll
+          for (int k = 0; k < KS; ++k) {
+            uint32_t x[4];
+            ldsm(x, kt + R::place(r, 2 * k + (lane >> 4)));
+            mma(c[0], x, qb[k][0][0], qb[k][0][1]);
+          }
         }
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          const int n = 2 * u16 + j;
-          if constexpr (kNarrow) {
-            const float2 ks = *reinterpret_cast<const float2*>(scales + 8 * n + 2 * t);
-            s[n][0] = (c[j][0] + c[j][2] * 0x1p-24f) * to_log2 * ks.x;
-            s[n][1] = (c[j][1] + c[j][3] * 0x1p-24f) * to_log2 * ks.y;
-          } else {
-            s[n][0] = c[j][0] * to_log2;
-            s[n][1] = c[j][1] * to_log2;
+          const float ks = kNarrow ? scales[u16 * 16 + 8 * j + g] : 1.f;
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float x = c[0][2 * j + e];
+            if constexpr (kNarrow && PACK) {  // the other part is two lanes away
+              const float y = __shfl_xor_sync(0xffffffffu, x, 2);
+              x = t < 2 ? x + y * 0x1p-24f : y + x * 0x1p-24f;
+            }
+            if constexpr (QP == 2) x += c[QP - 1][2 * j + e] * 0x1p-24f;
+            s[2 * u16 + j][e] = x * (to_log2[e] * ks);
           }
         }
       }
-      mask_scores(s, ring.exists(i), t);
+#pragma unroll
+      for (int j = 0; j < R::PL; ++j) {
+        const unsigned mask = ring.exists(i)[j];
+        if (mask != 0xffffffffu) {
+#pragma unroll
+          for (int n = 4 * j; n < (2 * SUB < 4 * j + 4 ? 2 * SUB : 4 * j + 4); ++n)
+            if (!((mask >> (8 * (n - 4 * j) + g)) & 1)) s[n][0] = s[n][1] = -INFINITY;
+        }
+      }
 
-      const float m_new = largest_score(s, m);
-      float base_w = finite_base(m_new);  // what the weights of the second product are relative to
+      float m_new[2], base[2], base_w[2];  // base_w: what the weights of the second product are relative to
+      largest_of(m_new, s, m);
+      base[0] = finite_base(m_new[0]), base[1] = finite_base(m_new[1]);
+      bool grown;
+      float grow[2];
       if constexpr (kNarrow) {
-        float lv[2 * SUB][2];
+        float sv[2 * SUB][2], z_new[2];
 #pragma unroll
         for (int n = 0; n < 2 * SUB; ++n) {
-          const float2 vs = *reinterpret_cast<const float2*>(scales + R::TP + 8 * n + 2 * t);
-          // within +-120, so that neither 2^(s - z) nor its product with v leaves fp32
-          lv[n][0] = s[n][0] + fminf(fmaxf(__log2f(fabsf(vs.x)), -120.f), 120.f);
-          lv[n][1] = s[n][1] + fminf(fmaxf(__log2f(fabsf(vs.y)), -120.f), 120.f);
+          const float lv = scales[2 * R::TP + 8 * n + g];
+          sv[n][0] = s[n][0] + lv, sv[n][1] = s[n][1] + lv;
         }
-        const float z_new = largest_score(lv, z);
-        base_w = finite_base(z_new) - 15.f;
-        if (__any_sync(0xffffffffu, z_new != z)) scale_all(o, pow2(z - finite_base(z_new)));
-        z = z_new;
+        largest_of(z_new, sv, z);
+        grown = z_new[0] != z[0] || z_new[1] != z[1];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          grow[e] = pow2(z[e] - finite_base(z_new[e]));
+          base_w[e] = finite_base(z_new[e]) - 15.f;
+          z[e] = z_new[e];
+        }
       } else {
-        if (__any_sync(0xffffffffu, m_new != m)) scale_all(o, pow2(m - base_w));
+        grown = m_new[0] != m[0] || m_new[1] != m[1];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) grow[e] = pow2(m[e] - base[e]), base_w[e] = base[e];
       }
-      const float base = finite_base(m_new);
-      l *= pow2(m - base);
-      m = m_new;
+      if (__any_sync(0xffffffffu, grown)) {
+#pragma unroll
+        for (int n = 0; n < KS; ++n)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) o[n][k] *= grow[k & 1];
+      }
+#pragma unroll
+      for (int e = 0; e < 2; ++e) l[e] *= pow2(m[e] - base[e]), m[e] = m_new[e];
+
 #pragma unroll
       for (int u16 = 0; u16 < SUB; ++u16) {
-        uint32_t pa[4];
+        uint32_t hi[2], lo[2];  // the second product's right side: weights of positions 2 t, 2 t + 1 (+ 8), column g
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
           const int n = 2 * u16 + j;
-          float x = pow2(s[n][0] - base), y = pow2(s[n][1] - base);
-          l += x + y;
+          float x = pow2(s[n][0] - base[0]), y = pow2(s[n][1] - base[1]);
+          l[0] += x, l[1] += y;
           if constexpr (kNarrow) {
-            const float2 vs = *reinterpret_cast<const float2*>(scales + R::TP + 8 * n + 2 * t);
-            x = pow2(s[n][0] - base_w) * vs.x, y = pow2(s[n][1] - base_w) * vs.y;
-            pa[2 * j] = pack_f16(x, y);
-            const float2 f = unpack_f16(pa[2 * j]);
-            pa[2 * j + 1] = pack_f16((x - f.x) * 0x1p11f, (y - f.y) * 0x1p11f);
+            const float vs = scales[R::TP + 8 * n + g];
+            x = pow2(s[n][0] - base_w[0]) * vs, y = pow2(s[n][1] - base_w[1]) * vs;
+          }
+          hi[j] = pack(x, y);
+          const float2 f = unpack(hi[j]);
+          lo[j] = pack(x - f.x, y - f.y);
+          if constexpr (PACK) {
+            hi[j] = transpose8(t < 2 ? hi[j] : lo[j]);
           } else {
-            const uint32_t hi = pack_bf16(x, y);
-            pa[2 * j] = hi;
-            pa[2 * j + 1] = pack_bf16(x - __uint_as_float(hi << 16), y - __uint_as_float(hi & 0xffff0000u));
+            hi[j] = transpose8(hi[j]), lo[j] = transpose8(lo[j]);
           }
         }
-        const int r = u16 * 16 + (lane & 15);
+        const int r = u16 * 16 + (kNarrow ? lane & 15 : (lane & 7) + (lane >> 4) * 8);
 #pragma unroll
         for (int c = 0; c < R::kChunks; c += 2) {
           uint32_t x[4];
-          ldsm_t(x, vt + R::place(r, c + (lane >> 4)));
+          ldsm_t(x, vt + R::place_v(r, c + (kNarrow ? lane >> 4 : (lane >> 3) & 1)));
+          if constexpr (kNarrow) {
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            if constexpr (kNarrow) {
-              uint32_t e0, e1, o0, o1;
-              codes_f16<true>(e0, o0, x[2 * j], C());
-              codes_f16<true>(e1, o1, x[2 * j + 1], C());
-              mma_f16(o[2 * (c + j)], pa[0], pa[1], pa[2], pa[3], e0, e1);
-              mma_f16(o[2 * (c + j) + 1], pa[0], pa[1], pa[2], pa[3], o0, o1);
-            } else {
-              mma_bf16(o[c + j], pa[0], pa[1], pa[2], pa[3], x[2 * j], x[2 * j + 1]);
+            for (int j = 0; j < 2; ++j) {  // rows g: elements 2 g of the chunk, rows g + 8: 2 g + 1
+              uint32_t f[4];
+              codes_f16<true>(f[0], f[1], x[2 * j], C());
+              codes_f16<true>(f[2], f[3], x[2 * j + 1], C());
+              mma(o[c + j], f, hi[0], hi[1]);
+              if constexpr (!PACK) mma(o[c + j], f, lo[0], lo[1]);
             }
+          } else {
+            mma(o[c / 2], x, hi[0], hi[1]);
+            if constexpr (!PACK) mma(o[c / 2], x, lo[0], lo[1]);
           }
         }
       }
     }
     cp_wait<0>();
-    l += __shfl_xor_sync(0xffffffffu, l, 1);
-    l += __shfl_xor_sync(0xffffffffu, l, 2);
     __syncthreads();  // all rings have been read
     Joint<D>& joint = *reinterpret_cast<Joint<D>*>(smem);
-    float* const row = joint.o[w][g];
-    if (t == 0) joint.m[w][g] = m, joint.l[w][g] = l;
-    if constexpr (kNarrow) {
-      const float f = pow2(finite_base(z) - finite_base(m) - 15.f), f2 = f * 0x1p-11f;
 #pragma unroll
-      for (int c = 0; c < NT / 2; ++c)
-        *reinterpret_cast<float4*>(row + 16 * c + 4 * t) =
-            make_float4(o[2 * c][0] * f + o[2 * c][2] * f2, o[2 * c + 1][0] * f + o[2 * c + 1][2] * f2,
-                        o[2 * c][1] * f + o[2 * c][3] * f2, o[2 * c + 1][1] * f + o[2 * c + 1][3] * f2);
-    } else {
+    for (int e = 0; e < 2; ++e) {
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
-        *reinterpret_cast<float2*>(row + 8 * n + 2 * t) = make_float2(o[n][0] + o[n][2], o[n][1] + o[n][3]);
+      for (int d = 4; d < 32; d <<= 1) l[e] += __shfl_xor_sync(0xffffffffu, l[e], d);
+      if (g == 0 && (!PACK || t < 2)) joint.m[w][2 * t + e] = m[e], joint.l[w][2 * t + e] = l[e];
+      const float f = kNarrow ? pow2(finite_base(z[e]) - finite_base(m[e]) - 15.f) : 1.f;
+#pragma unroll
+      for (int n = 0; n < KS; ++n) {
+        float x = o[n][e] * f, y = o[n][2 + e] * f;
+        if constexpr (PACK) x += __shfl_xor_sync(0xffffffffu, x, 2), y += __shfl_xor_sync(0xffffffffu, y, 2);
+        if (PACK && t >= 2) continue;
+        float* const row = joint.o[w][2 * t + e] + 16 * n;
+        if constexpr (kNarrow)
+          *reinterpret_cast<float2*>(row + 2 * g) = make_float2(x, y);
+        else
+          row[g] = x, row[g + 8] = y;
+      }
     }
     __syncthreads();
   }
@@ -913,14 +1005,18 @@ cudaError_t attn_e(const PagedAttnArgs& a, int* err, cudaStream_t s) {
   return e != cudaSuccess ? e : f;
 }
 
+template <typename T, typename C, int D>
+cudaError_t attn_h(const PagedAttnArgs& a, int* err, cudaStream_t s) {
+  return a.q_heads / a.pool.heads <= 4 ? attn_e<Half<T, C, D, true>, D>(a, err, s) : attn_e<Half<T, C, D, false>, D>(a, err, s);
+}
 template <typename C, int D>
 cudaError_t attn_d(int dt, const PagedAttnArgs& a, int* err, cudaStream_t s) {
   if constexpr (std::is_same<C, float>::value) {
     return attn_e<Full<D>, D>(a, err, s);
   } else {
     if constexpr (KvKind<C>::narrow)
-      if (dt == DT_F32) return attn_e<Half<float, C, D>, D>(a, err, s);
-    return attn_e<Half<bf16, C, D>, D>(a, err, s);
+      if (dt == DT_F32) return attn_h<float, C, D>(a, err, s);
+    return attn_h<bf16, C, D>(a, err, s);
   }
 }
 

@@ -371,6 +371,7 @@ struct KvPoolArgs {
   float *k_scale, *v_scale;
   long long page, head, row;                   // element strides
   long long scale_page, scale_head, scale_row;  // scale strides
+  uint32_t unit, page_u, head_u, row_u;         // the former in units of `unit` bytes, which 32 bits hold
   int kind, pages, rows, heads, dh;
   FastDiv div;  // by rows
 };

@@ -62,6 +62,18 @@ static int check_pool(const photon_kv_pages* p, int dtype, KvPoolArgs* out) {
       p->row_stride % per16)
     return refuse("pages: bases and strides must be multiples of 16 bytes");
   if (narrow && (!aligned_to(p->k_scale, 4) || !aligned_to(p->v_scale, 4))) return refuse("pages: scales not aligned");
+  if (p->page_stride < 0 || p->head_stride < 0 || p->row_stride < 0) return refuse("pages: negative stride");
+  // rows are found by 32-bit offsets in the largest power of two of bytes that divides every stride
+  const int64_t size = p->kind == PHOTON_KV_F32 ? 4 : p->kind == PHOTON_KV_BF16 ? 2 : 1, limit = INT64_MAX / 32;
+  if (p->page_stride > limit || p->head_stride > limit || p->row_stride > limit) return refuse("pages: stride out of range");
+  int64_t unit = 16;
+  while (unit < (1 << 20) && ((p->page_stride | p->head_stride | p->row_stride) * size) % (2 * unit) == 0) unit *= 2;
+  const double last = ((double)p->page_stride * (p->pages - 1) + (double)p->head_stride * (p->heads - 1) +
+                       (double)p->row_stride * (p->page_rows - 1)) * size / unit;
+  if (last >= 4294967295.0) return refuse("pages: too large for offsets in units of %d bytes", (int)unit);
+  out->unit = (uint32_t)unit;
+  out->page_u = (uint32_t)(p->page_stride * size / unit), out->head_u = (uint32_t)(p->head_stride * size / unit);
+  out->row_u = (uint32_t)(p->row_stride * size / unit);
   out->k = p->k, out->v = p->v;
   out->k_scale = narrow ? p->k_scale : nullptr;
   out->v_scale = narrow ? p->v_scale : nullptr;

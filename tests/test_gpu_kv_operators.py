@@ -14,10 +14,9 @@ value; a result stored as bf16 is off by another 2^-8 of itself.
   the sum that it is divided by is at least one, so an output loses at most
   2^-126 sum|v|.
 * Over 8-bit pages the weight of a position times its scale of V, c_t = w_t s_t, is
-  the sum of two fp16 numbers, c_t 2^15 / C = a + b 2^-11 with C a power of two at
-  most twice the largest c_t.  fp16's smallest step is 2^-24, so b is off by 2^-25
-  at most where it is too small for its 11 bits, and c_t by 2^-25 2^-11 2^-15 C =
-  2^-51 C <= 2^-50 max c_t: an output by 2^-50 max(c) sum|code|.
+  the sum of two fp16 numbers, c_t 2^15 / max(c) = a + b.  fp16's smallest step is
+  2^-24, so b is off by 2^-25 at most where it is too small for its 11 bits, and c_t
+  by 2^-40 max(c): an output by 2^-40 max(c) sum|code|, here doubled.
 """
 import math
 import threading
@@ -327,7 +326,7 @@ def attended(p, table, lens, q, window, scale):
         if p.k_scale is not None:
             vs = p.v_scale[page, :, row].double().T.repeat_interleave(G, 0)
             codes = V.abs() / vs.T.clamp(min=1e-300)[..., None]
-            bound[b] += 2.0 ** -50 * (w * vs).amax(-1)[:, None] * codes.sum(0)
+            bound[b] += 2.0 ** -39 * (w * vs).amax(-1)[:, None] * codes.sum(0)
         # log2 and its factor: 4 u of the larger of the maximum and the logarithm
         lse_bound[b] = ds[:, 0] + 4 * U + sums + 4 * U * (a.abs().amax(-1) + math.log(len(t)) + 1)
     return out, lse, bound, lse_bound
