@@ -30,68 +30,59 @@ __device__ __forceinline__ void turn(unsigned long long freq, int pos, float sca
   *c *= scale;
 }
 
-// The split of one tensor's rows [tokens][heads]: a block takes `tokens`
-// tokens, or one of `parts` spans of one token's rows.  `chunks` threads
-// share a row, always the same part of it, and the block's kThreads / chunks
-// groups take rows in turn.
+// The split of one tensor's rows [tokens][heads].  `chunks` threads share a
+// row, always the same part of it; a block's kThreads / chunks groups of them
+// take `hp` heads of `tp` tokens at a time, so that a thread stays with one
+// head and its addresses move by constants.  `parts` blocks share a token's
+// heads; a block takes `tokens` tokens.
 struct Split {
-  int heads, chunks, tokens, parts, span, blocks;
-  FastDiv by_heads, by_chunks, by_half, by_parts;
+  int heads, chunks, hp, tp, parts, tokens, blocks;
+  FastDiv by_chunks, by_hp, by_half, by_parts;
 };
 
-// work: threads' items in the whole launch.
+// work: threads' rows in the whole launch.
 Split split_rows(int n, int heads, int chunks, int rot, long long work) {
-  // four rows a group keep enough bytes in flight and share the block's
-  // angles; calls too small to give every SM two such blocks take one
   Split s = {};
   const int groups = kThreads / chunks;
   s.heads = heads, s.chunks = chunks;
-  s.span = work >= 2ll * 4 * kThreads * device_sm_count() ? 4 * groups : groups;
-  s.tokens = s.span / heads < 1 ? 1 : s.span / heads;
-  if (s.tokens > kTokensMax) s.tokens = kTokensMax;
-  if (rot && s.tokens > kAnglesMax / rot) s.tokens = kAnglesMax / rot;
-  if (s.tokens > n) s.tokens = n;
-  s.parts = s.tokens > 1 ? 1 : (heads + s.span - 1) / s.span;
-  if (s.parts == 1) s.span = s.tokens * heads;
+  // as few idle groups as up to four more blocks a token allow
+  const int least = (heads + groups - 1) / groups;
+  long long best = -1;
+  for (int parts = least; parts <= least + 4; ++parts) {
+    const int hp = (heads + parts - 1) / parts, tp = groups / hp;
+    const long long busy = (1ll << 20) * heads * tp / ((long long)parts * groups);
+    if (busy > best) best = busy, s.parts = parts, s.hp = hp, s.tp = tp;
+  }
+  // four rows a thread keep enough bytes in flight and share the block's
+  // angles; calls too small to give every SM two such blocks take one
+  s.tokens = work >= 2ll * 4 * kThreads * device_sm_count() ? 4 * s.tp : s.tp;
+  if (s.tokens > kTokensMax) s.tokens = kTokensMax / s.tp * s.tp;
+  if (rot && s.tokens > kAnglesMax / rot) s.tokens = kAnglesMax / rot / s.tp * s.tp;
   s.blocks = (n + s.tokens - 1) / s.tokens * s.parts;
-  s.by_heads = fast_div((uint32_t)heads);
   s.by_chunks = fast_div((uint32_t)chunks);
+  s.by_hp = fast_div((uint32_t)s.hp);
   s.by_half = fast_div(rot ? (uint32_t)rot / 2 : 1u);
   s.by_parts = fast_div((uint32_t)s.parts);
   return s;
 }
 
-// What a block does of it: tokens t0 .. t0 + n - 1, rows lo .. end - 1 of
-// theirs, `step` at a time; this thread the `mine`-th of them, part c.  The
-// loops run alike in all threads and guard the accesses, so that whole warps
-// meet in the shuffles.
+// What a block does of it: tokens t0 .. t0 + n - 1; this thread part c of one
+// head of every tp-th of them from `first` on.  The loops run alike in all
+// threads and guard the accesses, so that whole warps meet in the shuffles.
 struct Range {
-  int t0, n, lo, end, step, mine, c;
+  int t0, n, first, head, c;
+  bool active;
 };
 __device__ __forceinline__ Range range_of(const Split& s, int block, int tokens) {
   Range r;
   const int group = (int)div_fast((uint32_t)block, s.by_parts);
   r.t0 = group * s.tokens;
   r.n = min(s.tokens, tokens - r.t0);
-  r.step = (int)div_fast(kThreads, s.by_chunks);
-  r.mine = (int)div_fast(threadIdx.x, s.by_chunks);
-  r.c = threadIdx.x - r.mine * s.chunks;
-  r.lo = (block - group * s.parts) * s.span;
-  r.end = min(r.n * s.heads, r.lo + s.span);
-  return r;
-}
-// This thread's row of the group of rows from `lo` on; false: none.
-__device__ __forceinline__ bool row_at(const Range& r, int lo, int* i) {
-  *i = lo + r.mine;
-  return r.mine < r.step && *i < r.end;
-}
-struct Row {
-  int token, head;  // token within the block
-};
-__device__ __forceinline__ Row row_of(const Split& s, int i) {
-  Row r;
-  r.token = (int)div_fast((uint32_t)i, s.by_heads);
-  r.head = i - r.token * s.heads;
+  const int mine = (int)div_fast(threadIdx.x, s.by_chunks);
+  r.c = threadIdx.x - mine * s.chunks;
+  r.first = (int)div_fast((uint32_t)mine, s.by_hp);
+  r.head = (block - group * s.parts) * s.hp + (mine - r.first * s.hp);
+  r.active = r.first < s.tp && r.head < s.heads;
   return r;
 }
 
@@ -191,8 +182,8 @@ template <typename T, bool VEC>
 __device__ __forceinline__ void rotate_rows(float* angles, const RopeArgs& r, const int* pos, int n, int dh,
                                             const HeadsArgs& t, const Split& s, int block, bool back, bool padded) {
   const Range range = range_of(s, block, n);
-  const T* const in = (const T*)t.in + range.t0 * t.in_tok;
-  T* const out = (T*)t.out + range.t0 * t.out_tok;
+  const T* const in = (const T*)t.in + range.t0 * t.in_tok + range.head * t.in_head;
+  T* const out = (T*)t.out + range.t0 * t.out_tok + range.head * t.out_head;
   if constexpr (VEC) {
     constexpr int U = kAhead<T>;
     int e0, e1;
@@ -201,48 +192,43 @@ __device__ __forceinline__ void rotate_rows(float* angles, const RopeArgs& r, co
     auto fetch = [&](int lo) {
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        int i;
-        if (row_at(range, lo + u * range.step, &i)) {
-          const Row row = row_of(s, i);
-          const T* p = in + row.token * t.in_tok + row.head * t.in_head;
+        const int i = lo + u * s.tp + range.first;
+        if (range.active && i < range.n) {
+          const T* p = in + i * t.in_tok;
           x[u].load(p + e0), y[u].load(p + e1);
         }
       }
     };
-    fetch(range.lo);
+    fetch(0);
     fill_angles(angles, r, s, range, pos, back);
     __syncthreads();
-    for (int lo = range.lo; lo < range.end; lo += U * range.step) {
+    for (int lo = 0; lo < range.n; lo += U * s.tp) {
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        int i;
-        if (!row_at(range, lo + u * range.step, &i)) continue;
-        const Row row = row_of(s, i);
-        if (padded && pos[range.t0 + row.token] < 0) continue;
+        const int i = lo + u * s.tp + range.first;
+        if (!range.active || i >= range.n || (padded && pos[range.t0 + i] < 0)) continue;
         float v[8], w[8];
         x[u].get(v), y[u].get(w);
-        if (range.c < r.rot / 16) rotate16(v, w, range.c, angles + row.token * r.rot, r);
-        T* p = out + row.token * t.out_tok + row.head * t.out_head;
+        if (range.c < r.rot / 16) rotate16(v, w, range.c, angles + i * r.rot, r);
+        T* p = out + i * t.out_tok;
         store8<true>(p + e0, v);
         store8<true>(p + e1, w);
       }
-      fetch(lo + U * range.step);
+      fetch(lo + U * s.tp);
     }
   } else {
     fill_angles(angles, r, s, range, pos, back);
     __syncthreads();
-    for (int lo = range.lo; lo < range.end; lo += range.step) {
-      int i;
-      if (!row_at(range, lo, &i)) continue;
-      const Row row = row_of(s, i);
-      if (padded && pos[range.t0 + row.token] < 0) continue;
-      const T* p = in + row.token * t.in_tok + row.head * t.in_head;
-      T* o = out + row.token * t.out_tok + row.head * t.out_head;
+    if (!range.active) return;
+    for (int i = range.first; i < range.n; i += s.tp) {
+      if (padded && pos[range.t0 + i] < 0) continue;
+      const T* p = in + i * t.in_tok;
+      T* o = out + i * t.out_tok;
       for (int pair = range.c; pair < dh / 2; pair += s.chunks) {
         int e0, e1;
         pair_of(e0, e1, pair, r);
         float x = ld_f(p + e0), y = ld_f(p + e1);
-        const float* f = angles + row.token * r.rot + pair;
+        const float* f = angles + i * r.rot + pair;
         if (pair < r.rot / 2) rotate(x, y, f[0], f[r.rot / 2]);
         st_f(o + e0, x), st_f(o + e1, y);
       }
@@ -335,46 +321,44 @@ __global__ void __launch_bounds__(kThreads, 4) k_kv_write(const KvPoolArgs p, co
     return;
   }
   const Range range = range_of(sk, blockIdx.x, pl.tokens);
-  const T* const k_in = (const T*)k.in + range.t0 * k.in_tok;
-  const T* const v_in = (const T*)v.in + range.t0 * v.in_tok;
+  const T* const k_in = (const T*)k.in + range.t0 * k.in_tok + range.head * k.in_head;
+  const T* const v_in = (const T*)v.in + range.t0 * v.in_tok + range.head * v.in_head;
   Raw8<T> raw[4];
   int e0 = 0, e1 = 0;
   if constexpr (VEC) vectors_of(e0, e1, range.c, r.rot, p.dh);
   auto fetch = [&](int lo) {
-    int i;
-    if (VEC && row_at(range, lo, &i)) {
-      const Row row = row_of(sk, i);
-      const T* from = k_in + row.token * k.in_tok + row.head * k.in_head;
+    const int i = lo + range.first;
+    if (VEC && range.active && i < range.n) {
+      const T* from = k_in + i * k.in_tok;
       raw[0].load(from + e0), raw[1].load(from + e1);
-      from = v_in + row.token * v.in_tok + row.head * v.in_head;
+      from = v_in + i * v.in_tok;
       raw[2].load(from + e0), raw[3].load(from + e1);
     }
   };
-  fetch(range.lo);
+  fetch(0);
   if constexpr (ROPE) fill_angles(angles, r, sk, range, pl.pos, false);
   fill_places(places, p, pl, range, err);
   __syncthreads();
-  for (int lo = range.lo; lo < range.end; lo += range.step) {
-    int i;
-    const bool mine = row_at(range, lo, &i);
-    const Row row = row_of(sk, mine ? i : 0);
-    const long long at = places.at[row.token];
+  const long long head = range.head * p.head, scale_head = range.head * p.scale_head;
+  for (int lo = 0; lo < range.n; lo += sk.tp) {
+    const bool mine = range.active && lo + range.first < range.n;
+    const int i = mine ? lo + range.first : 0;
+    const long long at = places.at[i];
     const bool ok = mine && at >= 0;
 #pragma unroll
     for (int n = 0; n < 2; ++n) {  // k, v
       float x[8], y[8];
-      const float* f = angles + row.token * r.rot;
+      const float* f = angles + i * r.rot;
       if constexpr (VEC) {
         raw[2 * n].get(x), raw[2 * n + 1].get(y);
         if (ROPE && n == 0 && range.c < r.rot / 16) rotate16(x, y, range.c, f, r);
       } else {
-        const T* from = n ? v_in + row.token * v.in_tok + row.head * v.in_head
-                          : k_in + row.token * k.in_tok + row.head * k.in_head;
+        const T* from = n ? v_in + i * v.in_tok : k_in + i * k.in_tok;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           const int pair = 8 * range.c + j;
           pair_of(e0, e1, pair, r);
-          x[j] = ld_f(from + e0), y[j] = ld_f(from + e1);
+          x[j] = mine ? ld_f(from + e0) : 0.f, y[j] = mine ? ld_f(from + e1) : 0.f;
           if (ROPE && n == 0 && pair < r.rot / 2) rotate(x[j], y[j], f[pair], f[r.rot / 2 + pair]);
         }
       }
@@ -385,9 +369,9 @@ __global__ void __launch_bounds__(kThreads, 4) k_kv_write(const KvPoolArgs p, co
         else
           m = largest(x, y);
         const float scale = quantise16<C>(x, y, m, sk.chunks, range.c == 0);
-        if (ok && range.c == 0) (n ? p.v_scale : p.k_scale)[places.scale[row.token] + row.head * p.scale_head] = scale;
+        if (ok && range.c == 0) (n ? p.v_scale : p.k_scale)[places.scale[i] + scale_head] = scale;
       }
-      C* out = (C*)(n ? p.v : p.k) + at + row.head * p.head;
+      C* out = (C*)(n ? p.v : p.k) + at + head;
       if constexpr (VEC) {
         if (ok) store8<true>(out + e0, x), store8<true>(out + e1, y);
       } else {
@@ -398,7 +382,7 @@ __global__ void __launch_bounds__(kThreads, 4) k_kv_write(const KvPoolArgs p, co
         }
       }
     }
-    fetch(lo + range.step);
+    fetch(lo + sk.tp);
   }
 }
 
@@ -415,37 +399,34 @@ __global__ void __launch_bounds__(kThreads) k_kv_read(const KvPoolArgs p, const 
   fill_places(places, p, pl, range, err);
   __syncthreads();
   constexpr int U = kAhead<C>;
-  const C* const pages = (const C*)(value ? p.v : p.k) + 8 * range.c;
-  const float* const scales = value ? p.v_scale : p.k_scale;
-  T* const base = (T*)t.out + range.t0 * t.out_tok + 8 * range.c;
-  for (int lo = range.lo; lo < range.end; lo += U * range.step) {
+  const C* const pages = (const C*)(value ? p.v : p.k) + range.head * p.head + 8 * range.c;
+  const float* const scales = (value ? p.v_scale : p.k_scale) + range.head * p.scale_head;
+  T* const base = (T*)t.out + range.t0 * t.out_tok + range.head * t.out_head + 8 * range.c;
+  for (int lo = 0; lo < range.n; lo += U * s.tp) {
     Raw8<C> rx[U], ry[U];
     float scale[U];
-    T* out[U];
+    bool ok[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      int i;
-      const bool mine = row_at(range, lo + u * range.step, &i);
-      const Row row = row_of(s, mine ? i : 0);
-      const long long at = places.at[row.token];
-      out[u] = nullptr;
-      if (mine && at >= 0) {
-        out[u] = base + row.token * t.out_tok + row.head * t.out_head;
-        const C* in = pages + at + row.head * p.head;
+      const int i = lo + u * s.tp + range.first;
+      ok[u] = range.active && i < range.n && places.at[i] >= 0;
+      if (ok[u]) {
+        const C* in = pages + places.at[i];
         rx[u].load(in), ry[u].load(in + p.dh / 2);
-        if constexpr (KvKind<C>::narrow) scale[u] = scales[places.scale[row.token] + row.head * p.scale_head];
+        if constexpr (KvKind<C>::narrow) scale[u] = scales[places.scale[i]];
       }
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      if (!out[u]) continue;
+      if (!ok[u]) continue;
       float x[8], y[8];
       rx[u].get(x), ry[u].get(y);
       if constexpr (KvKind<C>::narrow) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) x[j] *= scale[u], y[j] *= scale[u];
       }
-      store8<VEC>(out[u], x), store8<VEC>(out[u] + p.dh / 2, y);
+      T* out = base + (lo + u * s.tp + range.first) * t.out_tok;
+      store8<VEC>(out, x), store8<VEC>(out + p.dh / 2, y);
     }
   }
 }
