@@ -26,6 +26,14 @@ static int result(cudaError_t e) {
 }
 static int launched() { return result(cudaGetLastError()); }
 
+// A process's first call may be a captured one: loading kernels and creating
+// the memory pool are no stream work, and are allowed during the call.
+struct RelaxedCapture {
+  cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+  RelaxedCapture() { cudaThreadExchangeStreamCaptureMode(&mode); }
+  ~RelaxedCapture() { cudaThreadExchangeStreamCaptureMode(&mode); }
+};
+
 static bool aligned_to(const void* p, size_t n) { return (uintptr_t)p % n == 0; }
 
 // Each check returns PHOTON_OK or the refusal.
@@ -176,6 +184,7 @@ int photon_rope(const photon_rope_args* args, void* stream) {
     CHECK(check_in_place(c.x2, c.y2));
     b = rows_of(&c.x2, &c.y2, c.heads2);
   }
+  RelaxedCapture relaxed;
   launch_rope(dt, r, c.d_pos, (int)c.tokens, (int)c.head_dim, rows_of(&c.x, &c.y, c.heads), b, c.backward != 0,
               (cudaStream_t)stream);
   return launched();
@@ -209,6 +218,7 @@ int photon_kv_write(const photon_kv_args* args, void* stream) {
   RopeArgs r;
   if (c.rope) CHECK(check_rope(c.rope, p.dh, &r));
   if (c.q_heads && !c.rope) return refuse("q is rotated, so it needs rope");
+  if (p.k == p.v || (p.k_scale && p.k_scale == p.v_scale)) return refuse("pages: keys and values share memory");
   if (!go) return PHOTON_OK;
   const int dt = (int)c.dtype;
   HeadsArgs q;
@@ -218,6 +228,7 @@ int photon_kv_write(const photon_kv_args* args, void* stream) {
     CHECK(check_in_place(c.q, c.q_out));
     q = rows_of(&c.q, &c.q_out, c.q_heads);
   }
+  RelaxedCapture relaxed;
   launch_kv_write(dt, p, pl, rows_of(&c.k, nullptr, p.heads), rows_of(&c.v, nullptr, p.heads), c.rope ? &r : nullptr, q,
                   c.d_err, (cudaStream_t)stream);
   return launched();
@@ -231,6 +242,7 @@ int photon_kv_read(const photon_kv_args* args, void* stream) {
   CHECK(check_kv(args, &p, &pl, &go));
   if (args->rope || args->q_heads) return refuse("a read takes no rope and no q");
   if (!go) return PHOTON_OK;
+  RelaxedCapture relaxed;
   launch_kv_read((int)args->dtype, p, pl, rows_of(nullptr, &args->k, p.heads), rows_of(nullptr, &args->v, p.heads),
                  args->d_err, (cudaStream_t)stream);
   return launched();
@@ -253,11 +265,13 @@ int photon_attn_decode_paged(const photon_attn_paged_args* args, void* stream) {
   if (!c.d_len || !aligned_to(c.d_len, 4)) return refuse("d_len: NULL or misaligned");
   CHECK(check_rows("q", (int)c.dtype, c.q.p));
   CHECK(check_rows("o", (int)c.dtype, c.o.p));
+  if (c.o.p == c.q.p) return refuse("o must not be q");
   if (!aligned_to(c.d_lse, 4) || !aligned_to(c.d_err, 4)) return refuse("d_lse, d_err: misaligned");
   a.table = c.d_table, a.table_stride = c.table_stride, a.seqs = (int)c.seqs, a.width = (int)c.width, a.len = c.d_len;
   a.q = c.q.p, a.q_seq = c.q.token, a.q_head = c.q.head, a.q_heads = (int)c.q_heads;
   a.window = (int)c.window, a.scale = scale;
   a.o = c.o.p, a.o_seq = c.o.token, a.o_head = c.o.head, a.lse = c.d_lse;
+  RelaxedCapture relaxed;
   return result(launch_attn_paged((int)c.dtype, a, c.d_err, (cudaStream_t)stream));
 }
 

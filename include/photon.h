@@ -727,11 +727,12 @@ typedef struct photon_kv_pages {
  * caller, set to a nonzero code by the kernels).
  *
  * photon_kv_write stores token t (k and v rows [heads][head_dim]) at position
- * d_pos[t] of sequence d_seq[t] (NULL: sequence t).  A negative position marks
+ * d_pos[t] of sequence d_seq[t] (NULL: sequence t); K, V, q_out and the inputs
+ * are distinct memory, but q_out may be q.  A negative position marks
  * padding: the token is left out.  The places of one call must be distinct (a
  * place named twice holds a mixture of the rows).  With `rope`, k is rotated
  * by its position first, in fp32, and q (q_heads heads, NULL and 0 for none)
- * is rotated into q_out (which may be q) in the same launch; q rows of padding
+ * is rotated into q_out in the same launch; q rows of padding
  * tokens are left as they were.  A narrow cache row gets the scale s =
  * max(amax, 1e-30) / top with amax its largest magnitude and top = 448 (E4M3)
  * or 127 (INT8), and the codes round(x * (top / max(amax, 1e-30))), to nearest
@@ -767,7 +768,10 @@ PHOTON_API int photon_kv_read(const photon_kv_args* args, void* stream);
  * A sequence without positions (length 0) gets o = 0 and lse = -infinity.
  * A length outside 0 .. width * page_rows is clamped to it and reported in
  * d_err, a page outside the pool leaves its positions out and is reported.
- * Softmax statistics and sums are fp32.  A call that splits long contexts over
+ * Softmax statistics and sums are fp32; o must not be q.  Rows behind a
+ * length, and pages that no position names, are never read, whatever they
+ * hold; an infinity or a NaN within the positions makes the outputs that it
+ * reaches infinite or NaN.  A call that splits long contexts over
  * the whole device takes its scratch from the library's stream-ordered pool
  * and returns it on the stream, as photon_attn_decode.  Errors: ERR_ARG, ERR_OOM, ERR_CUDA. */
 typedef struct photon_attn_paged_args {

@@ -19,6 +19,9 @@ value; a result stored as bf16 is off by another 2^-8 of itself.
   by 2^-40 max(c): an output by 2^-40 max(c) sum|code|, here doubled.
 """
 import math
+import os
+import subprocess
+import sys
 import threading
 
 import pytest
@@ -593,6 +596,63 @@ def test_graphs_and_streams(kind):
         del j["graph"]
 
 
+FIRST = """
+import sys, torch, hierarchical_autoregressive_lm_b200 as hal
+p = hal.KVPages.alloc(800, 16, 2, 64, torch.bfloat16)
+p.k.normal_(), p.v.normal_()
+table = torch.arange(800, dtype=torch.int32, device="cuda").view(1, 800)
+lens = torch.tensor([12000], dtype=torch.int32, device="cuda")
+q = torch.randn(1, 8, 64, device="cuda").bfloat16()
+a, b = torch.zeros_like(q), torch.zeros_like(q)
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    hal.attn_decode_paged(p, table, lens, q, a)
+g.replay()
+hal.attn_decode_paged(p, table, lens, q, b)
+torch.cuda.synchronize()
+assert torch.equal(a, b) and a.abs().max().item() > 0
+"""
+
+
+def test_first_call_is_a_captured_one():
+    run = subprocess.run([sys.executable, "-c", FIRST], capture_output=True, text=True, timeout=300,
+                         cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+    assert run.returncode == 0, run.stderr
+
+
+def test_out_of_memory_leaves_the_operators_usable():
+    g = gen(41)
+    lens = [40000]
+    p, table = paged(g, lens, 16, 1, 128, "bf16")
+    q = randn(g, 1, 4, 128).bfloat16()
+    good, _ = check_attention(p, table, lens, q)
+    out = torch.zeros_like(q)
+    hal.debug_fail_alloc(1)
+    try:
+        with pytest.raises(hal.PhotonError) as e:
+            hal.attn_decode_paged(p, table, ints(lens), q, out)
+        assert e.value.code == -2
+    finally:
+        hal.debug_fail_alloc(0)
+    hal.attn_decode_paged(p, table, ints(lens), q, out)
+    assert torch.equal(out, good)
+
+
+def test_one_table_row_for_several_sequences():
+    # a shared prompt: the table's rows are one row, the lengths differ
+    g = gen(43)
+    p, table = paged(g, [500], 16, 2, 64, "e4m3")
+    lens = [500, 17, 0, 333]
+    q = randn(g, 4, 6, 64).bfloat16()
+    shared = table.expand(4, -1)
+    check_attention(p, shared, lens, q)
+    pos, seq = ints([3, 3, 499, 3]), ints([0, 1, 2, 3])
+    k, v = (torch.empty(4, 2, 64, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    hal.kv_read(p, shared, pos, k, v, seq=seq)
+    assert torch.equal(k[0], k[1]) and torch.equal(v[0], v[3]) and not torch.equal(k[0], k[2])
+
+
 def test_calls_from_threads():
     """Eager calls of four threads on four streams give what each gives alone."""
     work = []
@@ -651,6 +711,10 @@ def test_binding_refusals():
         hal.attn_decode_paged(p, table, pos, q[:2], q[:2])
     with pytest.raises(hal.PhotonError, match="multiple of heads"):
         hal.attn_decode_paged(p, table, pos, q[:, :3], q[:, :3].clone())
+    with pytest.raises(hal.PhotonError, match="must not be q"):
+        hal.attn_decode_paged(p, table, pos, q, q)
+    with pytest.raises(hal.PhotonError, match="share memory"):
+        hal.kv_write(hal.KVPages(p.k, p.k), table, pos, k, k)
     with pytest.raises(hal.PhotonError, match="rot_dim"):
         hal.rope(hal.Rope(64), pos, k, k)
     with pytest.raises(ValueError, match="x2"):

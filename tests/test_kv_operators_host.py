@@ -13,7 +13,8 @@ import hierarchical_autoregressive_lm_b200 as hal
 
 getcontext().prec = 60
 PI = Decimal("3.14159265358979323846264338327950288419716939937510582097494")
-A = 1 << 20  # an aligned address that nothing reads
+A = 1 << 20  # aligned addresses that nothing reads
+B = 1 << 21
 
 
 def _turns(rot, theta=10000.0, scaling="none", factor=1.0, original_len=0, alpha=1.0, beta=32.0):
@@ -70,7 +71,7 @@ def test_rope_config_refusals():
 
 
 def _pages(**kw):
-    d = dict(k=A, v=A, k_scale=A, v_scale=A, page_stride=8 * 16 * 64, head_stride=16 * 64, row_stride=64, scale_page=8 * 16,
+    d = dict(k=A, v=B, k_scale=A, v_scale=B, page_stride=8 * 16 * 64, head_stride=16 * 64, row_stride=64, scale_page=8 * 16,
              scale_head=16, scale_row=1, kind=2, pages=10, page_rows=16, heads=8, head_dim=64)
     d.update(kw)
     return hal.photon_kv_pages(**d)
@@ -78,7 +79,8 @@ def _pages(**kw):
 
 BAD_PAGES = [dict(kind=4), dict(kind=-1), dict(kind=0), dict(pages=0), dict(page_rows=0), dict(heads=0), dict(head_dim=48),
              dict(k=None), dict(v=None), dict(k_scale=None), dict(v_scale=None), dict(k=A + 8), dict(page_stride=8 * 16 * 64 + 8),
-             dict(row_stride=72), dict(head_stride=-8), dict(k_scale=A + 2)]
+             dict(row_stride=72), dict(head_stride=-16), dict(k_scale=A + 2), dict(page_stride=1 << 40), dict(page_stride=16 + (1 << 36)),
+             dict(row_stride=1 << 62)]
 
 
 def _call(fn, cls, defaults, kw):
@@ -91,11 +93,11 @@ def _call(fn, cls, defaults, kw):
     return fn(ctypes.byref(a), None)
 
 
-ROWS, NONE = (A, 1024, 64), (None, 1024, 64)
+ROWS, OUT, NONE = (A, 1024, 64), (B, 1024, 64), (None, 1024, 64)
 
 
 def _attn(lib, pages, **kw):
-    d = dict(pages=pages, dtype=1, d_table=A, table_stride=4, seqs=2, width=4, d_len=A, q=ROWS, q_heads=16, window=0, scale=0.125, o=ROWS)
+    d = dict(pages=pages, dtype=1, d_table=A, table_stride=4, seqs=2, width=4, d_len=A, q=ROWS, q_heads=16, window=0, scale=0.125, o=OUT)
     return _call(lib.photon_attn_decode_paged, hal.photon_attn_paged_args, d, kw)
 
 
@@ -105,7 +107,7 @@ def test_attention_refusals():
         assert _attn(lib, _pages(**kw)) == -1, kw
         assert lib.photon_last_error() != b""
     for kw in (dict(dtype=2), dict(d_table=None), dict(seqs=-1), dict(width=0), dict(width=1 << 28), dict(width=1 << 40), dict(d_len=None),
-               dict(q=NONE), dict(o=NONE), dict(q_heads=12), dict(q_heads=0), dict(q_heads=1 << 40), dict(window=-1), dict(window=1 << 31),
+               dict(q=NONE), dict(o=NONE), dict(o=ROWS), dict(q_heads=12), dict(q_heads=0), dict(q_heads=1 << 40), dict(window=-1), dict(window=1 << 31),
                dict(scale=float("nan")), dict(scale=float("inf")), dict(scale=1e39), dict(q=(A + 1, 1024, 64)), dict(d_lse=A + 2),
                dict(d_err=A + 1), dict(d_table=A + 1), dict(seqs=1 << 28), dict(seqs=1 << 40)):
         assert _attn(lib, _pages(), **kw) == -1, kw
@@ -132,8 +134,8 @@ def test_write_and_read_refusals():
             assert lib.photon_last_error() != b""
         assert _call(fn, hal.photon_kv_args, dict(both, pages=pages), dict(tokens=0, d_pos=None, k=NONE, v=NONE, d_table=None)) == 0
     assert _call(lib.photon_kv_read, hal.photon_kv_args, dict(both, pages=pages), dict(rope=rope)) == -1
-    for kw in (dict(rope=hal.photon_rope_table(None, 64, 0, 1.0)), dict(rope=hal.photon_rope_table(A, 66, 0, 1.0)),
-               dict(rope=hal.photon_rope_table(A, 31, 0, 1.0)), dict(rope=rope, q_heads=16, q=ROWS),
+    for kw in (dict(pages=_pages(v=A)), dict(pages=_pages(v_scale=A)), dict(rope=hal.photon_rope_table(None, 64, 0, 1.0)),
+               dict(rope=hal.photon_rope_table(A, 66, 0, 1.0)), dict(rope=hal.photon_rope_table(A, 31, 0, 1.0)), dict(rope=rope, q_heads=16, q=ROWS),
                dict(rope=rope, q_heads=16, q_out=ROWS), dict(rope=rope, q=ROWS, q_out=(A, 2048, 64), q_heads=16)):
         assert _call(lib.photon_kv_write, hal.photon_kv_args, dict(both, pages=pages), kw) == -1, kw
 
