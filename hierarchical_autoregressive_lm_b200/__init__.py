@@ -723,25 +723,29 @@ def attn_decode_scratch_bytes(dtype_code: int, G: int, H: int, head_dim: int, ca
 # device, so the checks below take one short path and explain a refusal apart.
 
 _torch = None
-_raw_stream = None
+_raw_stream = _current_device = None
 
 
 def _need_torch():
-    global _torch, _raw_stream
+    global _torch, _raw_stream, _current_device
     if _torch is None:
         import torch
         _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
             lambda index: torch.cuda.current_stream(index).cuda_stream)
+        _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
         _torch = torch
     return _torch
 
 
 def _rows(t, dtype, shape: tuple, dev: int, name: str, out: bool = False) -> tuple:
     """Host-side check of a strided tensor of rows (last dimension contiguous) on device `dev`; its strides."""
-    if isinstance(t, _torch.Tensor) and t.dtype is dtype and t.shape == shape and t.get_device() == dev:
-        st = t.stride()
-        if (st[-1] == 1 or shape[-1] <= 1) and not (out and 0 in st):
-            return st
+    try:
+        if t.dtype is dtype and t.shape == shape and t.get_device() == dev:
+            st = t.stride()
+            if st[-1] == 1 and not (out and 0 in st):
+                return st
+    except (AttributeError, IndexError):
+        pass  # no tensor, or not of three dimensions
     if not isinstance(t, _torch.Tensor):
         raise TypeError(f"{name}: expected a torch tensor, got {type(t).__name__}")
     if t.dtype != dtype:
@@ -766,10 +770,13 @@ def _need_device(t, dev: int, name: str) -> None:
 
 def _flat(t, dtype, numel: int, dev: int, name: str) -> int:
     """Host-side check of a contiguous buffer of at least numel elements; its address."""
-    if not (isinstance(t, _torch.Tensor) and t.dtype is dtype and t.numel() >= numel and t.get_device() == dev
-            and t.is_contiguous()):
-        _need(t, dtype, numel, name)
-        _need_device(t, dev, name)
+    try:
+        if t.dtype is dtype and t.numel() >= numel and t.get_device() == dev and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _need(t, dtype, numel, name)
+    _need_device(t, dev, name)
     return t.data_ptr()
 
 
@@ -790,7 +797,7 @@ def _launch(fn, dev: int, stream, args: bytes) -> None:
         s = _raw_stream(dev)
     else:
         s = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-    if dev == _torch.cuda.current_device():
+    if dev == _current_device():
         rc = fn(args, s)
     else:
         with _torch.cuda.device(dev):
@@ -914,9 +921,9 @@ def rope(rope: Rope, pos, x, out, x2=None, out2=None, backward: bool = False, st
     if not isinstance(rope, Rope):
         raise TypeError(f"rope: expected Rope, got {type(rope).__name__}")
     code = _code(x, "x")
-    if x.dim() != 3:
-        raise ValueError("x: expected [tokens, heads, head_dim]")
     dtype, shape, dev = x.dtype, x.shape, x.get_device()
+    if len(shape) != 3:
+        raise ValueError("x: expected [tokens, heads, head_dim]")
     n, heads, dim = shape
     if dev < 0 or rope.freq.get_device() != dev:
         _need_device(x, dev, "x")

@@ -7,6 +7,12 @@
 // two vectors of eight that hold both elements of every pair, so that a
 // rotation needs no other thread's data and may run in place.
 //
+// Measured on a B200 (copy rate 6.54 TB/s): rotation of 8191 tokens, 40 heads
+// of 128, bf16: 28.0 us for 168 MB; 32255 tokens, 8 heads of 128, bf16 into
+// int8 pages: 39.0 us for 201 MB, as much bound by the instructions that
+// narrow 16 elements (about 200 a warp) as by bytes; 65536 tokens out of e4m3
+// pages: 64.2 us for 408 MB; 64 tokens, 32 heads of 64: 1.6 us.
+//
 // Angles.  A pair turns by pos * f turns, f a 64-bit binary fraction.  The
 // product modulo 2^64 drops whole turns without rounding; its upper 32 bits,
 // as a signed number of half-turns in [-1, 1), go to sincospif, whose
@@ -53,9 +59,12 @@ Split split_rows(int n, int heads, int chunks, int rot, long long work) {
     const long long busy = (1ll << 20) * heads * tp / ((long long)parts * groups);
     if (busy > best) best = busy, s.parts = parts, s.hp = hp, s.tp = tp;
   }
-  // four rows a thread keep enough bytes in flight and share the block's
-  // angles; calls too small to give every SM two such blocks take one
-  s.tokens = work >= 2ll * 4 * kThreads * device_sm_count() ? 4 * s.tp : s.tp;
+  // up to four rows a thread, which share the block's angles and keep bytes in
+  // flight, as long as one wave of blocks is full (us with one, two, four and
+  // six: rotation of 168 MB 37.5, 29.5, 28.2, 27.8; read of 408 MB 106, 77, 65,
+  // 66; write of 201 MB 43.5, 39.9, 39.1, 40.1)
+  const long long wave = 4ll * kThreads * device_sm_count();
+  s.tokens = (int)(work >= 4 * wave ? 4 : work <= wave ? 1 : (work + wave - 1) / wave) * s.tp;
   if (s.tokens > kTokensMax) s.tokens = kTokensMax / s.tp * s.tp;
   if (rot && s.tokens > kAnglesMax / rot) s.tokens = kAnglesMax / rot / s.tp * s.tp;
   s.blocks = (n + s.tokens - 1) / s.tokens * s.parts;
