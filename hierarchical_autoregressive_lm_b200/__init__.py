@@ -154,7 +154,7 @@ class photon_kv_args(ctypes.Structure):
 
 class photon_attn_paged_args(ctypes.Structure):
     _fields_ = _fields("pages:P d_table:P table_stride:q seqs:q width:q d_len:P dtype:q q_heads:q window:q q:R o:R "
-                       "d_lse:P d_err:P scale:d")
+                       "d_lse:P d_err:P scale:d d_scratch:P scratch_bytes:q")
 
 
 _pack_rope, _pack_kv, _pack_attn = (_packer(c).pack for c in (photon_rope_args, photon_kv_args, photon_attn_paged_args))
@@ -791,8 +791,8 @@ def _code(t, name: str) -> int:
     raise ValueError(f"{name}: expected torch.float32 or torch.bfloat16, got {dtype}")
 
 
-def _launch(fn, dev: int, stream, args: bytes) -> None:
-    """fn(args, stream) with device `dev` current."""
+def _launch(fn, dev: int, stream, args: bytes) -> int:
+    """fn(args, stream) with device `dev` current; what it returns, errors raised."""
     if stream is None:
         s = _raw_stream(dev)
     else:
@@ -802,8 +802,19 @@ def _launch(fn, dev: int, stream, args: bytes) -> None:
     else:
         with _torch.cuda.device(dev):
             rc = fn(args, s)
-    if rc:
+    if rc < 0:
         _check(rc)
+    return rc
+
+
+def _scratch(n: int, device, stream):
+    """n bytes for work on the stream, freed with the tensor in the stream's order."""
+    if stream is None:
+        return _torch.empty(n, dtype=_torch.uint8, device=device)
+    if not isinstance(stream, _torch.cuda.Stream):
+        stream = _torch.cuda.ExternalStream(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream), device)
+    with _torch.cuda.stream(stream):
+        return _torch.empty(n, dtype=_torch.uint8, device=device)
 
 
 class Rope:
@@ -1011,11 +1022,14 @@ def attn_decode_paged(pages: KVPages, table, lens, q, out, window: int = 0, scal
     shape = (seqs, heads, pages.head_dim)
     a, b = _rows(q, q.dtype, shape, dev, "q"), _rows(out, q.dtype, shape, dev, "out", True)
     i32 = _torch.int32
-    _launch(load_library().photon_attn_decode_paged, dev, stream,
-            _pack_attn(pages._ref, *place, _flat(lens, i32, seqs, dev, "lens"), code, heads, window, q.data_ptr(), a[0],
-                       a[1], out.data_ptr(), b[0], b[1],
-                       0 if lse is None else _flat(lse, _torch.float32, seqs * heads, dev, "lse"),
-                       0 if err is None else _flat(err, i32, 1, dev, "err"), pages._scale if scale is None else scale))
+    args = (pages._ref, *place, _flat(lens, i32, seqs, dev, "lens"), code, heads, window, q.data_ptr(), a[0], a[1],
+            out.data_ptr(), b[0], b[1], 0 if lse is None else _flat(lse, _torch.float32, seqs * heads, dev, "lse"),
+            0 if err is None else _flat(err, i32, 1, dev, "err"), pages._scale if scale is None else scale)
+    fn = load_library().photon_attn_decode_paged
+    need = _launch(fn, dev, stream, _pack_attn(*args, 0, -1))
+    if need:
+        scratch = _scratch(need, pages.device, stream)
+        _launch(fn, dev, stream, _pack_attn(*args, scratch.data_ptr(), need))
 
 
 def debug_fail_alloc(n: int) -> None:

@@ -396,6 +396,8 @@ struct PagedAttnArgs {
   void* o;
   long long o_seq, o_head;
   float* lse;
+  void* scratch;            // the caller's, if scratch_bytes > 0
+  long long scratch_bytes;  // 0: from scratch_malloc; below: say how many
 };
 void launch_rope(int dt, const RopeArgs& r, const int* pos, int tokens, int dh, const HeadsArgs& a,
                  const HeadsArgs& b, bool backward, cudaStream_t s);
@@ -403,8 +405,8 @@ void launch_kv_write(int dt, const KvPoolArgs& p, const KvPlaceArgs& pl, const H
                      const RopeArgs* r, const HeadsArgs& q, int* err, cudaStream_t s);
 void launch_kv_read(int dt, const KvPoolArgs& p, const KvPlaceArgs& pl, const HeadsArgs& k, const HeadsArgs& v,
                     int* err, cudaStream_t s);
-// Takes the scratch of its split from scratch_malloc and returns it on the stream.
-cudaError_t launch_attn_paged(int dt, const PagedAttnArgs& a, int* err, cudaStream_t s);
+// *need: the bytes of scratch a call without any needs; nothing was launched if that is not 0.
+cudaError_t launch_attn_paged(int dt, const PagedAttnArgs& a, int* err, cudaStream_t s, size_t* need);
 
 // Stream-ordered memory from the library's pool of the current device (runtime.cu); cudaFreeAsync returns it.
 cudaError_t scratch_malloc(void** p, size_t bytes, cudaStream_t s);

@@ -272,7 +272,12 @@ int photon_attn_decode_paged(const photon_attn_paged_args* args, void* stream) {
   a.window = (int)c.window, a.scale = scale;
   a.o = c.o.p, a.o_seq = c.o.token, a.o_head = c.o.head, a.lse = c.d_lse;
   RelaxedCapture relaxed;
-  return result(launch_attn_paged((int)c.dtype, a, c.d_err, (cudaStream_t)stream));
+  a.scratch = c.d_scratch, a.scratch_bytes = c.scratch_bytes;
+  if (c.scratch_bytes > 0 && (!c.d_scratch || !aligned_to(c.d_scratch, 16))) return refuse("d_scratch: NULL or misaligned");
+  size_t need = 0;
+  CHECK(result(launch_attn_paged((int)c.dtype, a, c.d_err, (cudaStream_t)stream, &need)));
+  if (need && c.scratch_bytes > 0) return refuse("scratch_bytes %lld, needs %zu", (long long)c.scratch_bytes, need);
+  return (int)need;
 }
 
 }  // extern "C"

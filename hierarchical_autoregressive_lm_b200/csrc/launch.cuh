@@ -75,10 +75,11 @@ __device__ __forceinline__ void pdl_trigger() {
 
 bool pdl_enabled();
 
-// `cluster` CTAs along x form a thread-block cluster (1: none).
+// `cluster` CTAs along x form a thread-block cluster (1: none); without
+// `early` the kernel starts after its predecessor's end.
 template <typename... KArgs, typename... Args>
 inline void launch_kernel_cluster(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem,
-                                  cudaStream_t s, int cluster, Args&&... args) {
+                                  cudaStream_t s, int cluster, bool early, Args&&... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = block;
@@ -92,7 +93,7 @@ inline void launch_kernel_cluster(void (*kernel)(KArgs...), dim3 grid, dim3 bloc
     attr[n].val.clusterDim.y = attr[n].val.clusterDim.z = 1;
     ++n;
   }
-  if (pdl_enabled()) {
+  if (early && pdl_enabled()) {
     attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[n].val.programmaticStreamSerializationAllowed = 1;
     ++n;
@@ -112,7 +113,7 @@ inline void launch_kernel_cluster(void (*kernel)(KArgs...), dim3 grid, dim3 bloc
 template <typename... KArgs, typename... Args>
 inline void launch_kernel(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem,
                           cudaStream_t s, Args&&... args) {
-  launch_kernel_cluster(kernel, grid, block, smem, s, 1, static_cast<Args&&>(args)...);
+  launch_kernel_cluster(kernel, grid, block, smem, s, 1, true, static_cast<Args&&>(args)...);
 }
 
 }  // namespace photon

@@ -771,9 +771,14 @@ PHOTON_API int photon_kv_read(const photon_kv_args* args, void* stream);
  * Softmax statistics and sums are fp32; o must not be q.  Rows behind a
  * length, and pages that no position names, are never read, whatever they
  * hold; an infinity or a NaN within the positions makes the outputs that it
- * reaches infinite or NaN.  A call that splits long contexts over
- * the whole device takes its scratch from the library's stream-ordered pool
- * and returns it on the stream, as photon_attn_decode.  Errors: ERR_ARG, ERR_OOM, ERR_CUDA. */
+ * reaches infinite or NaN.
+ * A call that splits long contexts over the whole device needs scratch of a
+ * size that its shapes decide (a few MB).  With scratch_bytes 0 the library
+ * takes it from its stream-ordered pool and returns it on the stream, as
+ * photon_attn_decode.  With scratch_bytes < 0 such a call launches nothing and
+ * returns the bytes it needs, a positive number; the caller repeats it with
+ * d_scratch of at least as many, which later work of the stream may reuse.
+ * Errors: ERR_ARG, ERR_OOM, ERR_CUDA. */
 typedef struct photon_attn_paged_args {
   const photon_kv_pages* pages;
   const int32_t* d_table; /* [seqs][width] */
@@ -784,6 +789,8 @@ typedef struct photon_attn_paged_args {
   float* d_lse;
   int32_t* d_err;
   double scale;
+  void* d_scratch; /* 16-byte aligned, or NULL */
+  int64_t scratch_bytes;
 } photon_attn_paged_args;
 PHOTON_API int photon_attn_decode_paged(const photon_attn_paged_args* args, void* stream);
 

@@ -18,6 +18,7 @@ value; a result stored as bf16 is off by another 2^-8 of itself.
   2^-24, so b is off by 2^-25 at most where it is too small for its 11 bits, and c_t
   by 2^-40 max(c): an output by 2^-40 max(c) sum|code|, here doubled.
 """
+import ctypes
 import math
 import os
 import subprocess
@@ -621,22 +622,40 @@ def test_first_call_is_a_captured_one():
     assert run.returncode == 0, run.stderr
 
 
-def test_out_of_memory_leaves_the_operators_usable():
+def test_scratch_of_the_library_and_of_the_caller():
+    """The C entry with scratch from its own pool (and with none to be had), and with the caller's."""
     g = gen(41)
     lens = [40000]
     p, table = paged(g, lens, 16, 1, 128, "bf16")
     q = randn(g, 1, 4, 128).bfloat16()
     good, _ = check_attention(p, table, lens, q)
-    out = torch.zeros_like(q)
+    out, n = torch.zeros_like(q), ints(lens)
+    fn = hal.load_library().photon_attn_decode_paged
+
+    def call(scratch, size):
+        a = hal.photon_attn_paged_args()
+        vals = dict(pages=p._ref, d_table=table.data_ptr(), table_stride=table.stride(0), seqs=1, width=table.shape[1], d_len=n.data_ptr(), dtype=1,
+                    q_heads=4, window=0, q=hal.photon_rows(q.data_ptr(), 512, 128), o=hal.photon_rows(out.data_ptr(), 512, 128), scale=128 ** -0.5,
+                    d_scratch=scratch, scratch_bytes=size)
+        for name, v in vals.items():
+            setattr(a, name, v)
+        rc = fn(ctypes.byref(a), torch.cuda.current_stream().cuda_stream)
+        torch.cuda.synchronize()
+        return rc
+
     hal.debug_fail_alloc(1)
     try:
-        with pytest.raises(hal.PhotonError) as e:
-            hal.attn_decode_paged(p, table, ints(lens), q, out)
-        assert e.value.code == -2
+        assert call(None, 0) == -2 and (out == 0).all()
     finally:
         hal.debug_fail_alloc(0)
-    hal.attn_decode_paged(p, table, ints(lens), q, out)
-    assert torch.equal(out, good)
+    assert call(None, 0) == 0 and torch.equal(out, good)
+    out.zero_()
+    need = call(None, -1)
+    assert 0 < need < 64 << 20 and (out == 0).all()
+    buf = torch.full((need + 64,), 255, dtype=torch.uint8, device="cuda")
+    assert call(buf.data_ptr() + 16, need - 1) == -1 and (out == 0).all()
+    assert call(buf.data_ptr() + 16, need) == 0 and torch.equal(out, good)
+    assert (buf[:16] == 255).all() and (buf[need + 16:] == 255).all()
 
 
 def test_one_table_row_for_several_sequences():
@@ -666,8 +685,8 @@ def test_calls_from_threads():
     torch.cuda.synchronize()
 
     def call(w):
-        for _ in range(20):
-            hal.attn_decode_paged(*w[:4], w[5], stream=w[6])
+        for i in range(20):
+            hal.attn_decode_paged(*w[:4], w[5], stream=w[6] if i % 2 else w[6].cuda_stream)
 
     threads = [threading.Thread(target=call, args=(w,)) for w in work]
     [t.start() for t in threads]

@@ -109,7 +109,7 @@ def test_attention_refusals():
     for kw in (dict(dtype=2), dict(d_table=None), dict(seqs=-1), dict(width=0), dict(width=1 << 28), dict(width=1 << 40), dict(d_len=None),
                dict(q=NONE), dict(o=NONE), dict(o=ROWS), dict(q_heads=12), dict(q_heads=0), dict(q_heads=1 << 40), dict(window=-1), dict(window=1 << 31),
                dict(scale=float("nan")), dict(scale=float("inf")), dict(scale=1e39), dict(q=(A + 1, 1024, 64)), dict(d_lse=A + 2),
-               dict(d_err=A + 1), dict(d_table=A + 1), dict(seqs=1 << 28), dict(seqs=1 << 40)):
+               dict(d_err=A + 1), dict(d_scratch=A + 8, scratch_bytes=1 << 20), dict(scratch_bytes=1 << 20), dict(d_table=A + 1), dict(seqs=1 << 28), dict(seqs=1 << 40)):
         assert _attn(lib, _pages(), **kw) == -1, kw
         assert lib.photon_last_error() != b""
     assert _attn(lib, None) == -1
