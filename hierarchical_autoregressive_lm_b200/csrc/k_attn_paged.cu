@@ -134,10 +134,10 @@ __device__ __forceinline__ void codes_f16(uint32_t& lo, uint32_t& hi, uint32_t w
   lo = *reinterpret_cast<const uint32_t*>(&x), hi = *reinterpret_cast<const uint32_t*>(&y);
 }
 
-// x as the sum of two tf32 numbers (the upper 19 bits of fp32), the first rounded, the second cut off.
+// x as the sum of two tf32 numbers (the upper 19 bits of fp32), both rounded.
 __device__ __forceinline__ void split_tf32(uint32_t& hi, uint32_t& lo, float x) {
   hi = (__float_as_uint(x) + 0x1000u) & 0xffffe000u;
-  lo = __float_as_uint(x - __uint_as_float(hi)) & 0xffffe000u;
+  lo = (__float_as_uint(x - __uint_as_float(hi)) + 0x1000u) & 0xffffe000u;
 }
 
 // What a unit's positions are.
@@ -546,9 +546,8 @@ struct Half {
 #pragma unroll
       for (int e = 0; e < 2; ++e) l[e] *= pow2(m[e] - base[e]), m[e] = m_new[e];
 
-#pragma unroll
-      for (int u16 = 0; u16 < SUB; ++u16) {
-        uint32_t hi[2], lo[2];  // the second product's right side: weights of positions 2 t, 2 t + 1 (+ 8), column g
+      // the second product's right side: weights of positions 2 t, 2 t + 1 (+ 8) of 16, column g
+      auto weights = [&](int u16, uint32_t (&hi)[2], uint32_t (&lo)[2]) {
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
           const int n = 2 * u16 + j;
@@ -567,24 +566,47 @@ struct Half {
             hi[j] = transpose8(hi[j]), lo[j] = transpose8(lo[j]);
           }
         }
+      };
+      // chunks c, c + 1 of 16 positions: two row tiles of 8-bit elements, one of bf16
+      auto product = [&](int u16, int c, const uint32_t (&hi)[2], const uint32_t (&lo)[2], float (*acc)[4]) {
         const int r = u16 * 16 + (kNarrow ? lane & 15 : (lane & 7) + (lane >> 4) * 8);
+        uint32_t x[4];
+        ldsm_t(x, vt + R::place_v(r, c + (kNarrow ? lane >> 4 : (lane >> 3) & 1)));
+        if constexpr (kNarrow) {
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {  // rows g: elements 2 g of the chunk, rows g + 8: 2 g + 1
+            uint32_t f[4];
+            codes_f16<true>(f[0], f[1], x[2 * j], C());
+            codes_f16<true>(f[2], f[3], x[2 * j + 1], C());
+            mma(acc[j], f, hi[0], hi[1]);
+            if constexpr (!PACK) mma(acc[j], f, lo[0], lo[1]);
+          }
+        } else {
+          mma(acc[0], x, hi[0], hi[1]);
+          if constexpr (!PACK) mma(acc[0], x, lo[0], lo[1]);
+        }
+      };
+      if constexpr (std::is_same<T, float>::value) {
+        // the tensor cores cut a sum off where an addition rounds it; fp32
+        // results get each tile's sum by an addition
+        uint32_t hi[SUB][2], lo[SUB][2];
+#pragma unroll
+        for (int u16 = 0; u16 < SUB; ++u16) weights(u16, hi[u16], lo[u16]);
 #pragma unroll
         for (int c = 0; c < R::kChunks; c += 2) {
-          uint32_t x[4];
-          ldsm_t(x, vt + R::place_v(r, c + (kNarrow ? lane >> 4 : (lane >> 3) & 1)));
-          if constexpr (kNarrow) {
+          float sum[2][4] = {};
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {  // rows g: elements 2 g of the chunk, rows g + 8: 2 g + 1
-              uint32_t f[4];
-              codes_f16<true>(f[0], f[1], x[2 * j], C());
-              codes_f16<true>(f[2], f[3], x[2 * j + 1], C());
-              mma(o[c + j], f, hi[0], hi[1]);
-              if constexpr (!PACK) mma(o[c + j], f, lo[0], lo[1]);
-            }
-          } else {
-            mma(o[c / 2], x, hi[0], hi[1]);
-            if constexpr (!PACK) mma(o[c / 2], x, lo[0], lo[1]);
-          }
+          for (int u16 = 0; u16 < SUB; ++u16) product(u16, c, hi[u16], lo[u16], sum);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) o[c + k / 4][k % 4] += sum[k / 4][k % 4];
+        }
+      } else {
+#pragma unroll
+        for (int u16 = 0; u16 < SUB; ++u16) {
+          uint32_t hi[2], lo[2];
+          weights(u16, hi, lo);
+#pragma unroll
+          for (int c = 0; c < R::kChunks; c += 2) product(u16, c, hi, lo, &o[kNarrow ? c : c / 2]);
         }
       }
     }
@@ -614,7 +636,10 @@ struct Half {
 };
 
 // fp32 pages: q, K, V and the weights each as the sum of two tf32 numbers
-// (m16n8k8), 21 bits of them; the products of the two smaller parts come along.
+// (m16n8k8), 22 bits of them; the products of the two smaller parts come along.
+// The tensor cores cut a sum off where an addition rounds it (8192 positions
+// of one sign in one accumulator came out 2^-16 too small), so their sums stay
+// short: a score's in three parts, an output's over a tile.
 template <int D>
 struct Full {
   using T = float;
@@ -652,7 +677,7 @@ struct Full {
     for (int i = 0; i < ring.mine; ++i) {
       ring.next(page, i);
       const uint32_t kt = ring.keys(i), vt = kt + R::kTile;
-      float c[N8][4] = {};
+      float c[N8][3][4] = {};  // of even and odd k steps, and of the smaller parts
 #pragma unroll
       for (int k = 0; k < KS; k += 2) {
         const uint4 q0 = qs[k * 32 + lane], q1 = qs[k * 32 + 32 + lane];
@@ -662,15 +687,18 @@ struct Full {
           ldsm(x, kt + R::place(8 * n + (lane & 7), 2 * k + (lane >> 3)));
 #pragma unroll
           for (int j = 0; j < 4; ++j) split_tf32(hi[j], lo[j], __uint_as_float(x[j]));
-          mma_tf32(c[n], q0.x, q0.y, q0.z, q0.w, hi[0], hi[1]);
-          mma_tf32(c[n], q0.x, q0.y, q0.z, q0.w, lo[0], lo[1]);
-          mma_tf32(c[n], q1.x, q1.y, q1.z, q1.w, hi[2], hi[3]);
-          mma_tf32(c[n], q1.x, q1.y, q1.z, q1.w, lo[2], lo[3]);
+          mma_tf32(c[n][0], q0.x, q0.y, q0.z, q0.w, hi[0], hi[1]);
+          mma_tf32(c[n][2], q0.x, q0.y, q0.z, q0.w, lo[0], lo[1]);
+          mma_tf32(c[n][1], q1.x, q1.y, q1.z, q1.w, hi[2], hi[3]);
+          mma_tf32(c[n][2], q1.x, q1.y, q1.z, q1.w, lo[2], lo[3]);
         }
       }
       float s[N8][2];
 #pragma unroll
-      for (int n = 0; n < N8; ++n) s[n][0] = (c[n][0] + c[n][2]) * to_log2, s[n][1] = (c[n][1] + c[n][3]) * to_log2;
+      for (int n = 0; n < N8; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          s[n][e] = (c[n][0][e] + c[n][1][e] + (c[n][2][e] + (c[n][0][2 + e] + c[n][1][2 + e] + c[n][2][2 + e]))) * to_log2;
       mask_scores(s, ring.exists(i), t);
       const float m_new = largest_score(s, m), base = finite_base(m_new);
       if (__any_sync(0xffffffffu, m_new != m)) {
@@ -679,24 +707,28 @@ struct Full {
         scale_all(o, grow);
       }
       m = m_new;
+      uint32_t pa[N8][4];  // k t of the product is position 2 t, k t + 4 is position 2 t + 1
 #pragma unroll
       for (int n = 0; n < N8; ++n) {
         const float x = pow2(s[n][0] - base), y = pow2(s[n][1] - base);
         l += x + y;
-        // k t of the product is position 2 t, k t + 4 is position 2 t + 1
-        uint32_t pa[4];
-        split_tf32(pa[0], pa[1], x);
-        split_tf32(pa[2], pa[3], y);
-        const int r = 8 * n + 2 * t;
+        split_tf32(pa[n][0], pa[n][1], x);
+        split_tf32(pa[n][2], pa[n][3], y);
+      }
 #pragma unroll
-        for (int d = 0; d < NT; ++d) {
-          const int chunk = 2 * d + (g >> 2);
+      for (int d = 0; d < NT; ++d) {
+        float sum[4] = {};
+#pragma unroll
+        for (int n = 0; n < N8; ++n) {
+          const int r = 8 * n + 2 * t, chunk = 2 * d + (g >> 2);
           uint32_t h0, h1, l0, l1;
           split_tf32(h0, l0, ld_shared(vt + R::place_v(r, chunk) + (g & 3) * 4));
           split_tf32(h1, l1, ld_shared(vt + R::place_v(r + 1, chunk) + (g & 3) * 4));
-          mma_tf32(o[d], pa[0], pa[1], pa[2], pa[3], h0, h1);
-          mma_tf32(o[d], pa[0], pa[1], pa[2], pa[3], l0, l1);
+          mma_tf32(sum, pa[n][0], pa[n][1], pa[n][2], pa[n][3], h0, h1);
+          mma_tf32(sum, pa[n][0], pa[n][1], pa[n][2], pa[n][3], l0, l1);
         }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) o[d][k] += sum[k];
       }
     }
     cp_wait<0>();

@@ -448,6 +448,30 @@ def test_attention_unusual_values(dtype, kind):
     assert torch.equal(out[4, 0], base[4, 0]) and out[4, 1].isnan().all()
 
 
+@pytest.mark.parametrize("kind", ["fp32", "e4m3", "int8"])
+@pytest.mark.parametrize("dim", [32, 64, 128, 256])
+def test_attention_long_sums_have_no_direction(kind, dim):
+    """Even weights over values of one sign, thousands of positions to a sum.
+
+    Sums that cut off where they should round come out too small by half a step a
+    position.  A tile's sum (64 positions, two terms each, at most 16 steps of the
+    tensor cores) may lose 16 u; the tiles' sums are rounded to nearest, without a
+    direction: the errors' mean stays below 16 u, while 4096 / (4 * 8) steps cut off
+    would take it to 64 u.
+    """
+    g = gen(47)
+    lens = [4096] * 64
+    p, table = paged(g, lens, 64, 8, dim, kind)
+    p.v.copy_((p.v.float().abs() + 1).clamp(max=TOP.get(kind, 9.0)).to(p.v.dtype))
+    for s in (p.k_scale, p.v_scale):
+        if s is not None:
+            s.fill_(2.0 ** -7)
+    q = randn(g, 64, 8, dim) * 0.01
+    out, _ = check_attention(p, table, lens, q, dtype="fp32")
+    want = attended(p, table, lens[:4], q[:4], 0, dim ** -0.5)[0]
+    assert abs(((out[:4].double() - want) / want).mean().item()) <= 16 * U
+
+
 @pytest.mark.parametrize("kind", ["bf16", "e4m3"])
 def test_attention_weights_far_apart(kind):
     # a position that takes nearly all the weight with small values, beside others with large ones
