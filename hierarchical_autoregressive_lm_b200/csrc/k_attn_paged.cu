@@ -22,10 +22,10 @@
 // Which one a call takes: see choose().
 //
 // Measured on a B200 (copy rate 6.54 TB/s): 64 sequences of 512 to 4096
-// positions, 32 heads over 8 of 128, bf16 pages: 96 us for 605 MB (6.3 TB/s).
-// Two of 131072, e4m3 pages: 93 us for 554 MB (5.9 TB/s; the tile's
+// positions, 32 heads over 8 of 128, bf16 pages: 95 us for 605 MB (6.3 TB/s).
+// Two of 131072, e4m3 pages: 92 us for 554 MB (6.0 TB/s; the tile's
 // instructions and the products' latency take the rest).  fp32 pages, 1024
-// units of 4096 positions of 64: 322 us for 2.15 GB.  One sequence of 257
+// units of 4096 positions of 64: 340 us for 2.15 GB.  One sequence of 257
 // positions, 16 heads of 64: 4.3 us, the latency of length, table, rows and join.
 #include <cmath>
 #include <type_traits>
@@ -336,11 +336,12 @@ __device__ __forceinline__ void scale_all(float (&o)[N][4], float f) {
 //
 // 8-bit pages: both products run in fp16, which holds every code exactly.  q
 // is divided by the power of two at its largest element; what fp16 cannot
-// hold of it follows times 2^24, so q keeps 22 bits.  A weight times its
-// scale v has fp32's range, which fp16 has not: w = 2^(15 + s - z) |v|, with a
-// running maximum z of s + log2 |v| of its own, is at most 2^15, and what fp16
-// cannot hold of it follows.  Weights keep 22 bits down to 2^-17 of the
-// largest, and steps of 2^-39 of the largest below that.
+// hold of it follows times 2^24, so q keeps 22 bits.  A weight p times its
+// scale v has fp32's range, which fp16 has not: p v 2^(15 - x), with a power of
+// two 2^x above every p |v| so far (x = ceil(z - m) for the running maximum z
+// of s + log2 |v|), is at most 2^15, and what fp16 cannot hold of it follows.
+// Weights keep 22 bits down to 2^-17 of the largest, and steps of 2^-38 of the
+// largest below that.
 template <typename T_, typename C, int D, bool PACK>
 struct Half {
   using T = T_;
@@ -438,8 +439,8 @@ struct Half {
 #pragma unroll
       for (int e = 0; e < 2; ++e) to_log2[e] = __shfl_sync(0xffffffffu, f, (2 * t + e) * 4);
     }
-    // columns 2 t, 2 t + 1: maxima of s and of s + log2 |v|, sums; rows g, g + 8 of the row tiles
-    float m[2] = {-INFINITY, -INFINITY}, z[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, o[KS][4];
+    // columns 2 t, 2 t + 1: maxima of s and of s + log2 |v|, x, sums; rows g, g + 8 of the row tiles
+    float m[2] = {-INFINITY, -INFINITY}, z[2] = {-INFINITY, -INFINITY}, x2[2] = {0.f, 0.f}, l[2] = {0.f, 0.f}, o[KS][4];
 #pragma unroll
     for (int n = 0; n < KS; ++n)
 #pragma unroll
@@ -450,7 +451,7 @@ struct Half {
       const uint32_t kt = ring.keys(i), vt = kt + R::kTile;
       const float* const scales = ring.scales(i);
       if constexpr (kNarrow) {
-        // log2 |v| of every position, within +-120, so that neither 2^(s - z) nor its product with v leaves fp32
+        // log2 |v| of every position, within +-120, so that no power of two leaves fp32
 #pragma unroll
         for (int j = 0; j < R::PL; ++j)
           if (j * 32 + lane < R::TP) {
@@ -512,11 +513,9 @@ struct Half {
         }
       }
 
-      float m_new[2], base[2], base_w[2];  // base_w: what the weights of the second product are relative to
+      float m_new[2], base[2], grow[2], up[2];  // up: 2^(15 - x)
+      bool grown = false;
       largest_of(m_new, s, m);
-      base[0] = finite_base(m_new[0]), base[1] = finite_base(m_new[1]);
-      bool grown;
-      float grow[2];
       if constexpr (kNarrow) {
         float sv[2 * SUB][2], z_new[2];
 #pragma unroll
@@ -525,17 +524,21 @@ struct Half {
           sv[n][0] = s[n][0] + lv, sv[n][1] = s[n][1] + lv;
         }
         largest_of(z_new, sv, z);
-        grown = z_new[0] != z[0] || z_new[1] != z[1];
+        z[0] = z_new[0], z[1] = z_new[1];
+      }
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          grow[e] = pow2(z[e] - finite_base(z_new[e]));
-          base_w[e] = finite_base(z_new[e]) - 15.f;
-          z[e] = z_new[e];
+      for (int e = 0; e < 2; ++e) {
+        base[e] = finite_base(m_new[e]);
+        float moved = m[e] - base[e];
+        if constexpr (kNarrow) {
+          const float x = fminf(fmaxf(ceilf(z[e] - base[e]), -110.f), 121.f);
+          up[e] = __int_as_float((142 - (int)x) << 23);
+          moved += x2[e] - x;
+          grown |= x != x2[e];
+          x2[e] = x;
         }
-      } else {
-        grown = m_new[0] != m[0] || m_new[1] != m[1];
-#pragma unroll
-        for (int e = 0; e < 2; ++e) grow[e] = pow2(m[e] - base[e]), base_w[e] = base[e];
+        grown |= m_new[e] != m[e];
+        grow[e] = pow2(moved);
       }
       if (__any_sync(0xffffffffu, grown)) {
 #pragma unroll
@@ -555,7 +558,7 @@ struct Half {
           l[0] += x, l[1] += y;
           if constexpr (kNarrow) {
             const float vs = scales[R::TP + 8 * n + g];
-            x = pow2(s[n][0] - base_w[0]) * vs, y = pow2(s[n][1] - base_w[1]) * vs;
+            x = x * vs * up[0], y = y * vs * up[1];
           }
           hi[j] = pack(x, y);
           const float2 f = unpack(hi[j]);
@@ -618,7 +621,7 @@ struct Half {
 #pragma unroll
       for (int d = 4; d < 32; d <<= 1) l[e] += __shfl_xor_sync(0xffffffffu, l[e], d);
       if (g == 0 && (!PACK || t < 2)) joint.m[w][2 * t + e] = m[e], joint.l[w][2 * t + e] = l[e];
-      const float f = kNarrow ? pow2(finite_base(z[e]) - finite_base(m[e]) - 15.f) : 1.f;
+      const float f = kNarrow ? __int_as_float((112 + (int)x2[e]) << 23) : 1.f;  // 2^(x - 15)
 #pragma unroll
       for (int n = 0; n < KS; ++n) {
         float x = o[n][e] * f, y = o[n][2 + e] * f;

@@ -14,9 +14,10 @@ value; a result stored as bf16 is off by another 2^-8 of itself.
   the sum that it is divided by is at least one, so an output loses at most
   2^-126 sum|v|.
 * Over 8-bit pages the weight of a position times its scale of V, c_t = w_t s_t, is
-  the sum of two fp16 numbers, c_t 2^15 / max(c) = a + b.  fp16's smallest step is
-  2^-24, so b is off by 2^-25 at most where it is too small for its 11 bits, and c_t
-  by 2^-40 max(c): an output by 2^-40 max(c) sum|code|, here doubled.
+  the sum of two fp16 numbers, c_t 2^15 / C = a + b with C a power of two at most
+  twice max(c).  fp16's smallest step is 2^-24, so b is off by 2^-25 at most where it
+  is too small for its 11 bits, and c_t by 2^-40 C: an output by 2^-39 max(c)
+  sum|code|.
 """
 import ctypes
 import math
