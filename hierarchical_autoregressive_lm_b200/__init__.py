@@ -724,15 +724,19 @@ def attn_decode_scratch_bytes(dtype_code: int, G: int, H: int, head_dim: int, ca
 
 _torch = None
 _raw_stream = _current_device = None
+_codes: dict = {}
 
 
 def _need_torch():
+    """Torch and the library, for the handles of these operators."""
     global _torch, _raw_stream, _current_device
+    load_library()
     if _torch is None:
         import torch
         _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
             lambda index: torch.cuda.current_stream(index).cuda_stream)
         _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+        _codes.update({torch.float32: 0, torch.bfloat16: 1})
         _torch = torch
     return _torch
 
@@ -782,10 +786,9 @@ def _flat(t, dtype, numel: int, dev: int, name: str) -> int:
 
 def _code(t, name: str) -> int:
     dtype = getattr(t, "dtype", None)
-    if dtype is _torch.bfloat16:
-        return 1
-    if dtype is _torch.float32:
-        return 0
+    code = _codes.get(dtype)
+    if code is not None:
+        return code
     if not isinstance(t, _torch.Tensor):
         raise TypeError(f"{name}: expected a torch tensor, got {type(t).__name__}")
     raise ValueError(f"{name}: expected torch.float32 or torch.bfloat16, got {dtype}")
@@ -841,7 +844,7 @@ class Rope:
         # a copy from pageable memory has arrived when it returns: ready for every stream
         self.freq = torch.frombuffer(self._host, dtype=torch.int64).to(device)
         self._t = photon_rope_table(self.freq.data_ptr(), self.rot_dim, int(self.interleaved), self.scale)
-        self._ref = ctypes.addressof(self._t)
+        self._ref, self._dev = ctypes.addressof(self._t), self.freq.get_device()
 
     @property
     def turns(self) -> list:
@@ -936,22 +939,23 @@ def rope(rope: Rope, pos, x, out, x2=None, out2=None, backward: bool = False, st
     if len(shape) != 3:
         raise ValueError("x: expected [tokens, heads, head_dim]")
     n, heads, dim = shape
-    if dev < 0 or rope.freq.get_device() != dev:
+    if dev < 0 or rope._dev != dev:
         _need_device(x, dev, "x")
         _need_device(rope.freq, dev, "rope")
     a, b = _rows(x, dtype, shape, dev, "x"), _rows(out, dtype, shape, dev, "out", True)
     p2 = o2 = heads2 = 0
     a2 = b2 = (0, 0)
     if x2 is not None:
-        if not isinstance(x2, _torch.Tensor) or x2.dim() != 3:
+        shape = getattr(x2, "shape", ())
+        if len(shape) != 3:
             raise ValueError("x2: expected [tokens, heads, head_dim]")
-        heads2 = x2.shape[1]
+        heads2 = shape[1]
         shape = (n, heads2, dim)
         a2, b2 = _rows(x2, dtype, shape, dev, "x2"), _rows(out2, dtype, shape, dev, "out2", True)
         p2, o2 = x2.data_ptr(), out2.data_ptr()
     elif out2 is not None:
         raise ValueError("out2 without x2")
-    _launch(load_library().photon_rope, dev, stream,
+    _launch(_lib.photon_rope, dev, stream,
             _pack_rope(rope._ref, _flat(pos, _torch.int32, n, dev, "pos"), code, n, dim, int(backward), x.data_ptr(),
                        a[0], a[1], out.data_ptr(), b[0], b[1], heads, p2, a2[0], a2[1], o2, b2[0], b2[1], heads2))
 
@@ -983,7 +987,7 @@ def kv_write(pages: KVPages, table, pos, k, v, seq=None, rope: Rope = None, q=No
     if rope is not None:
         if not isinstance(rope, Rope):
             raise TypeError(f"rope: expected Rope, got {type(rope).__name__}")
-        if rope.freq.get_device() != dev:
+        if rope._dev != dev:
             _need_device(rope.freq, dev, "rope")
         ref = rope._ref
     if q is not None:
@@ -997,7 +1001,7 @@ def kv_write(pages: KVPages, table, pos, k, v, seq=None, rope: Rope = None, q=No
         qp, op = q.data_ptr(), q_out.data_ptr()
     elif q_out is not None:
         raise ValueError("q_out without q")
-    _launch(load_library().photon_kv_write, dev, stream,
+    _launch(_lib.photon_kv_write, dev, stream,
             _pack_kv(*args, ref, qp, a[0], a[1], op, b[0], b[1], heads))
 
 
@@ -1005,7 +1009,7 @@ def kv_read(pages: KVPages, table, pos, k, v, seq=None, stream=None, err=None) -
     """photon_kv_read: copies the places kv_write would write into k, v [tokens, heads,
     head_dim] (code * scale of an 8-bit cache); rows of padding tokens are left as they were."""
     args = _places(pages, table, pos, seq, k, v, True, err)
-    _launch(load_library().photon_kv_read, pages._dev, stream, _pack_kv(*args, 0, 0, 0, 0, 0, 0, 0, 0))
+    _launch(_lib.photon_kv_read, pages._dev, stream, _pack_kv(*args, 0, 0, 0, 0, 0, 0, 0, 0))
 
 
 def attn_decode_paged(pages: KVPages, table, lens, q, out, window: int = 0, scale: Optional[float] = None, lse=None,
@@ -1025,7 +1029,7 @@ def attn_decode_paged(pages: KVPages, table, lens, q, out, window: int = 0, scal
     args = (pages._ref, *place, _flat(lens, i32, seqs, dev, "lens"), code, heads, window, q.data_ptr(), a[0], a[1],
             out.data_ptr(), b[0], b[1], 0 if lse is None else _flat(lse, _torch.float32, seqs * heads, dev, "lse"),
             0 if err is None else _flat(err, i32, 1, dev, "err"), pages._scale if scale is None else scale)
-    fn = load_library().photon_attn_decode_paged
+    fn = _lib.photon_attn_decode_paged
     need = _launch(fn, dev, stream, _pack_attn(*args, 0, -1))
     if need:
         scratch = _scratch(need, pages.device, stream)
