@@ -703,7 +703,9 @@ PHOTON_API int photon_rope(const photon_rope_args* args, void* stream);
  * element (page, head, row, e) of K and of V sits at page * page_stride +
  * head * head_stride + row * row_stride + e, so that both [pages][heads]
  * [page_rows][head_dim] and [pages][page_rows][heads][head_dim] fit.  Bases
- * and strides are multiples of 16 bytes.  A narrow kind holds one fp32 scale
+ * and strides are multiples of 16 bytes, strides not negative; the pool spans
+ * less than 2^32 times the largest power of two of bytes that divides every
+ * stride (64 GB at least).  A narrow kind holds one fp32 scale
  * per (page, head, row) of K and of V beside its codes; an element's value
  * is code * scale. */
 enum { PHOTON_KV_F32 = 0, PHOTON_KV_BF16 = 1, PHOTON_KV_E4M3 = 2, PHOTON_KV_INT8 = 3 };

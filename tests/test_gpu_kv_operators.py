@@ -564,6 +564,28 @@ def test_offsets_past_32_bits():
     check_attention(p, table, [n], randn(g, 1, 4 * H, dim).bfloat16())
 
 
+@pytest.mark.parametrize("kind", ["bf16", "int8"])
+def test_largest_tables_and_most_sequences(kind):
+    # 2^30 positions of room, a length that ends in the second page of a million rows
+    g = gen(53)
+    p = filled(g, 3, 1, 1 << 20, 32, kind)
+    table = torch.full((2, 1024), -1, dtype=torch.int32, device="cuda")
+    table[0, :2], table[1, 0] = ints([2, 0]), 1
+    check_attention(p, table, [(1 << 20) + 77, 3], randn(g, 2, 4, 32).bfloat16())
+    check_attention(p, table, [(1 << 20) + 77, 1 << 20], randn(g, 2, 4, 32).bfloat16(), window=1000)
+    err = ints([0])
+    k = randn(g, 2, 1, 32).bfloat16()
+    hal.kv_write(p, table, ints([(1 << 20) + 77, (1 << 20) - 1]), k, k.clone(), err=err)
+    hal.kv_write(p, table, ints([(1 << 30) - 1, -1]), k, k.clone(), err=err)  # no page there
+    assert err.item() != 0
+    # thousands of short sequences, some empty, over uneven groups
+    lens = torch.randint(0, 70, (3000,), generator=g, device="cuda").tolist()
+    p, table = paged(g, lens, 5, 3, 64, kind)
+    check_attention(p, table, lens, randn(g, 3000, 15, 64).bfloat16())
+    p, table = paged(g, [900], 32, 128, 256, kind)
+    check_attention(p, table, [900], randn(g, 1, 128, 256).bfloat16())
+
+
 def test_no_tokens():
     p = pool(2, 1, 4, 32, "bf16")
     x, i = torch.empty(0, 1, 32, dtype=torch.bfloat16, device="cuda"), ints([])
