@@ -8,10 +8,10 @@
 // rotation needs no other thread's data and may run in place.
 //
 // Measured on a B200 (copy rate 6.54 TB/s): rotation of 8191 tokens, 40 heads
-// of 128, bf16: 28.0 us for 168 MB; 32255 tokens, 8 heads of 128, bf16 into
-// int8 pages: 39.0 us for 201 MB, as much bound by the instructions that
+// of 128, bf16: 27.1 us for 168 MB; 32255 tokens, 8 heads of 128, bf16 into
+// int8 pages: 38.7 us for 201 MB, as much bound by the instructions that
 // narrow 16 elements (about 200 a warp) as by bytes; 65536 tokens out of e4m3
-// pages: 64.2 us for 408 MB; 64 tokens, 32 heads of 64: 1.6 us.
+// pages: 64.6 us for 408 MB; 64 tokens, 32 heads of 64: 1.5 us.
 //
 // Angles.  A pair turns by pos * f turns, f a 64-bit binary fraction.  The
 // product modulo 2^64 drops whole turns without rounding; its upper 32 bits,
@@ -25,9 +25,14 @@ namespace photon {
 
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kTokensMax = 256;   // of a block
-constexpr int kAnglesMax = 4096;  // sines and cosines of a block
+// Small blocks: a block's rows wait for its places and angles, and the more
+// blocks an SM holds the less that shows (rotation of 168 MB, 64 tokens into
+// e4m3: 27.1 and 2.6 us with 128 threads, 28.0 and 2.9 with 256, 31.4 and 3.5
+// with 512).
+constexpr int kThreads = 128;
+constexpr int kBlocks = 8;                    // an SM holds of them
+constexpr int kTokensMax = 256;               // of a block
+constexpr int kAnglesMax = 16 * kThreads;     // sines and cosines of a block: one token for every row it takes at a time
 
 __device__ __forceinline__ void turn(unsigned long long freq, int pos, float scale, float* s, float* c) {
   const int half_turns = (int)(((unsigned long long)(long long)pos * freq) >> 32);
@@ -61,9 +66,9 @@ Split split_rows(int n, int heads, int chunks, int rot, long long work) {
   }
   // up to four rows a thread, which share the block's angles and keep bytes in
   // flight, as long as one wave of blocks is full (us with one, two, four and
-  // six: rotation of 168 MB 37.5, 29.5, 28.2, 27.8; read of 408 MB 106, 77, 65,
-  // 66; write of 201 MB 43.5, 39.9, 39.1, 40.1)
-  const long long wave = 4ll * kThreads * device_sm_count();
+  // six, in blocks of 256: rotation of 168 MB 37.5, 29.5, 28.2, 27.8; read of
+  // 408 MB 106, 77, 65, 66; write of 201 MB 43.5, 39.9, 39.1, 40.1)
+  const long long wave = (long long)kBlocks * kThreads * device_sm_count();
   s.tokens = (int)(work >= 4 * wave ? 4 : work <= wave ? 1 : (work + wave - 1) / wave) * s.tp;
   if (s.tokens > kTokensMax) s.tokens = kTokensMax / s.tp * s.tp;
   if (rot && s.tokens > kAnglesMax / rot) s.tokens = kAnglesMax / rot / s.tp * s.tp;
@@ -247,7 +252,7 @@ __device__ __forceinline__ void rotate_rows(float* angles, const RopeArgs& r, co
 
 // Blocks below sa.blocks take rows of a, the others of b.
 template <typename T, bool VEC>
-__global__ void __launch_bounds__(kThreads, 4) k_rope(const RopeArgs r, const int* __restrict__ pos, int n, int dh,
+__global__ void __launch_bounds__(kThreads, kBlocks) k_rope(const RopeArgs r, const int* __restrict__ pos, int n, int dh,
                                                       const HeadsArgs a, const HeadsArgs b, bool back, const Split sa,
                                                       const Split sb) {
   __shared__ __align__(16) float angles[kAnglesMax];
@@ -318,7 +323,7 @@ __device__ __forceinline__ uint32_t largest(const Raw8<bf16>& x, const Raw8<bf16
 // Blocks below sk.blocks take rows of k and v, which share a place, the
 // others rows of q, which are rotated into q.out.
 template <typename T, typename C, bool VEC, bool ROPE>
-__global__ void __launch_bounds__(kThreads, 4) k_kv_write(const KvPoolArgs p, const KvPlaceArgs pl, const HeadsArgs k,
+__global__ void __launch_bounds__(kThreads, kBlocks) k_kv_write(const KvPoolArgs p, const KvPlaceArgs pl, const HeadsArgs k,
                                                           const HeadsArgs v, const RopeArgs r, const HeadsArgs q,
                                                           const Split sk, const Split sq, int* err) {
   __shared__ __align__(16) float angles[ROPE ? kAnglesMax : 1];
