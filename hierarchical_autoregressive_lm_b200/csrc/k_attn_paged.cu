@@ -134,10 +134,18 @@ __device__ __forceinline__ void codes_f16(uint32_t& lo, uint32_t& hi, uint32_t w
   lo = *reinterpret_cast<const uint32_t*>(&x), hi = *reinterpret_cast<const uint32_t*>(&y);
 }
 
-// x as the sum of two tf32 numbers (the upper 19 bits of fp32), both rounded.
+// x as the sum of two tf32 numbers (the upper 19 bits of fp32): the first is
+// rounded, what it leaves is at most 2^12 units of x's last place, so that
+// cutting it to 11 bits drops one unit at most, and has either sign.  Rounding
+// by an addition carries a NaN's bits anywhere, but the remainder of what is
+// not finite is NaN, and stays one.  Numbers that would round to infinity are
+// cut off; SMALL: there are none.
+template <bool SMALL = false>
 __device__ __forceinline__ void split_tf32(uint32_t& hi, uint32_t& lo, float x) {
-  hi = (__float_as_uint(x) + 0x1000u) & 0xffffe000u;
-  lo = (__float_as_uint(x - __uint_as_float(hi)) + 0x1000u) & 0xffffe000u;
+  uint32_t up = __float_as_uint(x);
+  if (SMALL || fabsf(x) < __uint_as_float(0x7f7ff000u)) up += 0x1000u;
+  hi = up & 0xffffe000u;
+  lo = __float_as_uint(x - __uint_as_float(hi)) & 0xffffe000u;
 }
 
 // What a unit's positions are.
@@ -715,8 +723,8 @@ struct Full {
       for (int n = 0; n < N8; ++n) {
         const float x = pow2(s[n][0] - base), y = pow2(s[n][1] - base);
         l += x + y;
-        split_tf32(pa[n][0], pa[n][1], x);
-        split_tf32(pa[n][2], pa[n][3], y);
+        split_tf32<true>(pa[n][0], pa[n][1], x);  // at most 1
+        split_tf32<true>(pa[n][2], pa[n][3], y);
       }
 #pragma unroll
       for (int d = 0; d < NT; ++d) {

@@ -449,6 +449,79 @@ def test_attention_unusual_values(dtype, kind):
     assert torch.equal(out[4, 0], base[4, 0]) and out[4, 1].isnan().all()
 
 
+# NaNs by their bits: what GPU arithmetic makes, the same with a sign, others whose payload is all in the upper or in the lower bits
+NANS = [0x7fffffff, 0xffffffff, 0x7ffff000, 0xfffff000, 0x7fc00000, 0x7f800001, 0xff801fff]
+
+
+@pytest.mark.parametrize("dim", [32, 64, 128, 256])
+@pytest.mark.parametrize("bits", NANS)
+def test_attention_keeps_every_nan(dim, bits):
+    g = gen(61)
+    lens = [50, 50, 50, 1500, 1500]
+    p, table = paged(g, lens, 16, 1, dim, "fp32")
+    q = randn(g, 5, 3, dim)
+    base, base_lse = check_attention(p, table, lens, q, dtype="fp32")
+
+    def poison(t):
+        t.view(torch.int32).fill_(bits - (1 << 32) if bits >> 31 else bits)
+
+    poison(p.k[table[0, 1].item(), 0, 3, 5:6])
+    poison(p.v[table[1, 1].item(), 0, 3, 5:6])
+    poison(q[2, 1, 7:8])
+    poison(p.k[table[3, 70].item(), 0, 2, 9:10])
+    out, lse = torch.empty_like(q), torch.empty(5, 3, device="cuda")
+    hal.attn_decode_paged(p, table, ints(lens), q, out, lse=lse)
+    assert out[0].isnan().all() and lse[0].isnan().all() and out[3].isnan().all() and lse[3].isnan().all()
+    assert out[1, :, 5].isnan().all() and torch.equal(lse[1], base_lse[1])
+    assert torch.equal(out[1, :, :5], base[1, :, :5]) and torch.equal(out[1, :, 6:], base[1, :, 6:])
+    assert out[2, 1].isnan().all() and lse[2, 1].isnan().all()
+    for h in (0, 2):
+        assert torch.equal(out[2, h], base[2, h]) and torch.equal(lse[2, h], base_lse[2, h])
+    assert torch.equal(out[4], base[4]) and torch.equal(lse[4], base_lse[4])
+
+
+@pytest.mark.parametrize("dtype,kind", KINDS)
+@pytest.mark.parametrize("x", [math.nan, math.inf, -math.inf])
+def test_a_nan_of_the_rotation_reaches_the_attention(dtype, kind, x):
+    # the rotation turns what is not finite into the NaN of GPU arithmetic
+    g = gen(67)
+    B, H, G, dim, rows, n = 3, 2, 3, 64, 8, 20
+    p = pool(B * 4, H, rows, dim, kind)
+    table = torch.arange(B * 4, device="cuda", dtype=torch.int32).view(B, 4)
+    r = hal.Rope(dim)
+    seq, pos = torch.arange(B, device="cuda").repeat_interleave(n).int(), torch.arange(n, device="cuda").repeat(B).int()
+    q, k, v = (randn(g, B * n, h, dim).to(DT[dtype]) for h in (H * G, H, H))
+    k[2 * n // 3, 0, 1] = k[2 * n // 3, 0, 1 + dim // 2] = x  # a pair of sequence 0, key head 0
+    q[2 * n - 1, 1, 2] = q[2 * n - 1, 1, 2 + dim // 2] = x    # the last token of sequence 1, head 1
+    out_q = torch.empty_like(q)
+    hal.kv_write(p, table, pos, k, v, seq=seq, rope=r, q=q, q_out=out_q)
+    last = out_q[n - 1::n]
+    out, lse = torch.empty_like(last), torch.empty(B, H * G, device="cuda")
+    hal.attn_decode_paged(p, table, ints([n] * B), last, out, lse=lse)
+    bad = torch.zeros(B, H * G, dtype=torch.bool, device="cuda")
+    bad[0, :G], bad[1, 1] = True, True
+    assert out[bad].isnan().all() and lse[bad].isnan().all()
+    assert out[~bad].isfinite().all() and lse[~bad].isfinite().all()
+
+
+@pytest.mark.parametrize("dim", [32, 64, 128, 256])
+def test_attention_largest_finite_numbers(dim):
+    # next to fp32's largest number a rounding to fewer bits would leave the finite ones
+    g = gen(71)
+    lens = [1, 40, 1]
+    p, table = paged(g, lens, 8, 1, dim, "fp32")
+    top = torch.finfo(torch.float32).max
+    q = randn(g, 3, 2, dim)
+    p.v[table[0, 0].long(), 0, 0, ::2] = top
+    p.v[table[0, 0].long(), 0, 0, 1::2] = -top * (1 - 2.0 ** -12)
+    p.k[table[1, 2].long(), 0, 3] = -top
+    q[1] = 0
+    p.k[table[2, 0].long(), 0, 0] = torch.arange(dim, device="cuda") % 3 - 1.0
+    q[2] = 0
+    q[2, 0, 1], q[2, 1, 2] = 7, top / 4
+    check_attention(p, table, lens, q, dtype="fp32", scale=2.0 ** -120)
+
+
 @pytest.mark.parametrize("kind", ["fp32", "e4m3", "int8"])
 @pytest.mark.parametrize("dim", [32, 64, 128, 256])
 def test_attention_long_sums_have_no_direction(kind, dim):
