@@ -109,7 +109,8 @@ __global__ void __launch_bounds__(32 * W, (QMAX == 1 ? PHOTON_DEC_RESIDENT_WARPS
   // is written at the end of a step, long before this kernel's predecessor
   // (the projection that writes this step's queries and new keys) runs.  So
   // the first ring stages, when they hold only such keys, are copied before
-  // waiting for the predecessor.  The position is read again after the wait;
+  // waiting for the predecessor (kv_ready; a caller's buffers may hold what
+  // the predecessor writes).  The position is read again after the wait;
   // if it moved (its writer was the predecessor after all), the early copies
   // are drained and the plan starts over.
   int p0 = a.p0_dev ? (__ldcg(a.p0_dev) + a.p0) : a.p0;
@@ -159,11 +160,20 @@ __global__ void __launch_bounds__(32 * W, (QMAX == 1 ? PHOTON_DEC_RESIDENT_WARPS
   int pre = 0;
   {
     const int nb0 = (kw1 - kw0 + STEP - 1) / STEP;
-    for (int st = 0; st < kDecStages - 1 && st < nb0; ++st) {
+    for (int st = 0; a.kv_ready && st < kDecStages - 1 && st < nb0; ++st) {
       if (min(kw1, kw0 + (st + 1) * STEP) > p0) break;
       issue(st, kw0 + st * STEP);
       cp_async_commit_group();
       ++pre;
+    }
+    if (!a.kv_ready && lane == 0 && kw0 < kw1) {
+      // rows that the predecessor may be writing come as far as L2, where its
+      // stores land: no value is read before the wait (a chain of calls on 64
+      // sequences, 16 heads, 272 keys: 13.7 us a call with the copies, 14.4 so,
+      // 16.1 without; one, three, four and all stages 14.9, 15.1, 15.8, 17.8)
+      const uint32_t bytes = (uint32_t)(min(kw1 - kw0, (kDecStages - 1) * STEP) * DH * (int)sizeof(T));
+      ptx::bulk_prefetch_l2(kown + (long long)kw0 * DH, bytes);
+      ptx::bulk_prefetch_l2(vown + (long long)kw0 * DH, bytes);
     }
   }
   pdl_wait();  // the predecessor's queries and new keys are visible from here on

@@ -57,7 +57,7 @@ __global__ void __launch_bounds__(128, 1)
     k_gemm_tc(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
               int M, int N, int nkb, int kb_per_split, Epilogue ep, float* __restrict__ part,
               int* __restrict__ tile_count, const char* __restrict__ w_ptr, long long w_ld_bytes,
-              int* err) {
+              bool w_ready, int* err) {
   using Cfg = TcCfg<BN, STAGES>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -102,11 +102,12 @@ __global__ void __launch_bounds__(128, 1)
   const uint32_t tmem = *tmem_slot;
   // Everything above touched only shared/tensor memory and the kernel's
   // own parameters.  Activations are read and outputs written only after the
-  // previous kernel in the stream has completed (pdl_wait).  The weight
-  // operand is never written by any kernel, so the producer fetches the
-  // weight tiles of the first ring stages before waiting: with programmatic
-  // dependent launch that streaming overlaps the previous kernel's tail.
-  if (threadIdx.x != 0) pdl_wait();
+  // previous kernel in the stream has completed (pdl_wait).  A weight operand
+  // that no kernel writes (w_ready) does not depend on it, so the producer
+  // fetches the weight tiles of the first ring stages before waiting: with
+  // programmatic dependent launch that streaming overlaps the previous
+  // kernel's tail.
+  if (threadIdx.x != 0 || !w_ready) pdl_wait();
   pdl_trigger();
 
   if (threadIdx.x == 0) {
@@ -849,7 +850,7 @@ template <int BN, int S, int STAGES, bool NORM>
 __global__ void __launch_bounds__(kDecThreads, 1)
     k_gemm_dec(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
                int M, int N, int nkb, int kbs, Epilogue ep, const float* __restrict__ nx,
-               long long nldx, const float* __restrict__ ng, float eps, int* err) {
+               long long nldx, const float* __restrict__ ng, float eps, bool w_ready, int* err) {
   using Cfg = DecCfg<BN, STAGES, NORM>;
   constexpr int LDP = BN + 4;  // partial-tile row stride in floats (16-byte skew per row)
   static_assert(128 * LDP * 4 <= Cfg::kDataBytes, "the partial tile reuses the data region");
@@ -914,9 +915,9 @@ __global__ void __launch_bounds__(kDecThreads, 1)
   ptx::tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   DEC_TRACE(1);
-  // weights are never written by any kernel: the producer starts on them
-  // before waiting for the previous kernel (see k_gemm_tc)
-  if (threadIdx.x != 0) pdl_wait();
+  // weights that are ready: the producer starts on them before waiting for
+  // the previous kernel (see k_gemm_tc)
+  if (threadIdx.x != 0 || !w_ready) pdl_wait();
   pdl_trigger();
 
   // ---- epilogue items of this thread (warps 2-7): (RoPE pair, token quad)
@@ -1318,7 +1319,7 @@ bool make_map(CUtensorMap* m, const void* ptr, long long rows, int K, long long 
 template <int BN, int STAGES, bool SWAP, bool SAMPLE = false>
 void run_tc(const CUtensorMap& ma, const CUtensorMap& mb, int grid_a, int grid_b, int splits,
             int M, int N, int nkb, int kbs, const Epilogue& ep, float* part, int* counters,
-            const void* w_ptr, long long w_ld_bytes, int* err, cudaStream_t s) {
+            const void* w_ptr, long long w_ld_bytes, bool w_ready, int* err, cudaStream_t s) {
   using Cfg = TcCfg<BN, STAGES>;
   static PerDevice configured;
   configured.get([] {
@@ -1328,7 +1329,7 @@ void run_tc(const CUtensorMap& ma, const CUtensorMap& mb, int grid_a, int grid_b
   });
   dim3 grid(grid_a, grid_b, splits);
   launch_kernel(k_gemm_tc<BN, STAGES, SWAP, SAMPLE>, grid, 128, Cfg::kSmemBytes, s, ma, mb, M, N, nkb, kbs,
-                ep, part, counters, static_cast<const char*>(w_ptr), w_ld_bytes, err);
+                ep, part, counters, static_cast<const char*>(w_ptr), w_ld_bytes, w_ready, err);
 }
 
 template <int BN, int STAGES, bool SAMPLE = false>
@@ -1457,7 +1458,7 @@ void run_dec(const CUtensorMap& mw, const CUtensorMap& mx, int ga, int gb, const
   cfg.attrs = attr;
   cfg.numAttrs = n;
   cudaLaunchKernelEx(&cfg, k_gemm_dec<BN, S, STAGES, NORM>, mw, mx, a.M, a.N, a.K / kBK, kbs, a.ep,
-                     a.norm_x, a.norm_ld, a.norm_g, a.norm_eps, err);
+                     a.norm_x, a.norm_ld, a.norm_g, a.norm_eps, a.w_ready, err);
   note_launch();
 }
 
@@ -1769,11 +1770,11 @@ bool launch_gemm_tc(const GemmArgs& a, const GemmWorkspace& ws, int* err, cudaSt
   if (p.swap) {
     if (!make_map(&ma, a.W, N, K, a.ldw, kBM) || !make_map(&mb, a.A, M, K, a.lda, p.bn)) return false;
     if (p.bn == 64)
-      run_tc<64, 8, true>(ma, mb, p.ga, p.gb, p.splits, M, N, nkb, p.kbs, a.ep, part, counters, a.W, a.ldw * 2, err, s);
+      run_tc<64, 8, true>(ma, mb, p.ga, p.gb, p.splits, M, N, nkb, p.kbs, a.ep, part, counters, a.W, a.ldw * 2, a.w_ready, err, s);
     else if (p.bn == 128)
-      run_tc<128, 4, true>(ma, mb, p.ga, p.gb, p.splits, M, N, nkb, p.kbs, a.ep, part, counters, a.W, a.ldw * 2, err, s);
+      run_tc<128, 4, true>(ma, mb, p.ga, p.gb, p.splits, M, N, nkb, p.kbs, a.ep, part, counters, a.W, a.ldw * 2, a.w_ready, err, s);
     else
-      run_tc<256, 4, true>(ma, mb, p.ga, p.gb, p.splits, M, N, nkb, p.kbs, a.ep, part, counters, a.W, a.ldw * 2, err, s);
+      run_tc<256, 4, true>(ma, mb, p.ga, p.gb, p.splits, M, N, nkb, p.kbs, a.ep, part, counters, a.W, a.ldw * 2, a.w_ready, err, s);
   } else {
     if (!make_map(&ma, a.A, M, K, a.lda, kBM) || !make_map(&mb, a.W, N, K, a.ldw, p.bn)) return false;
     if (a.ep.ssq_in != nullptr && !(p.splits == 1 && p.ga * p.gb >= persist_min_tiles() && persistent_enabled()))
@@ -1798,14 +1799,14 @@ bool launch_gemm_tc(const GemmArgs& a, const GemmWorkspace& ws, int* err, cudaSt
     }
     if (p.bn == 256)
       sample ? run_tc<256, 4, false, true>(ma, mb, p.ga, p.gb, p.splits, M, N, nkb, p.kbs, a.ep, part, counters,
-                                           a.W, a.ldw * 2, err, s)
+                                           a.W, a.ldw * 2, a.w_ready, err, s)
              : run_tc<256, 4, false>(ma, mb, p.ga, p.gb, p.splits, M, N, nkb, p.kbs, a.ep, part, counters, a.W,
-                                     a.ldw * 2, err, s);
+                                     a.ldw * 2, a.w_ready, err, s);
     else
       sample ? run_tc<128, 4, false, true>(ma, mb, p.ga, p.gb, p.splits, M, N, nkb, p.kbs, a.ep, part, counters,
-                                           a.W, a.ldw * 2, err, s)
+                                           a.W, a.ldw * 2, a.w_ready, err, s)
              : run_tc<128, 4, false>(ma, mb, p.ga, p.gb, p.splits, M, N, nkb, p.kbs, a.ep, part, counters, a.W,
-                                     a.ldw * 2, err, s);
+                                     a.ldw * 2, a.w_ready, err, s);
   }
   return true;
 }

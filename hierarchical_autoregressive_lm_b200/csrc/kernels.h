@@ -95,6 +95,10 @@ struct GemmArgs {
   long long norm_ld = 0;
   const float* norm_g = nullptr;
   float norm_eps = 0.f;
+  // W was written before the preceding kernel of the stream started (a
+  // model's weights): its first tiles may be fetched while that kernel still
+  // runs.  False for a caller's W, which that kernel may be writing.
+  bool w_ready = true;
 };
 
 // Scratch the GEMM may use for split-K: fp32 partial tiles, and one counter
@@ -140,6 +144,10 @@ struct AttnArgs {
   // table or a page outside the arrays reads row 0 of page 0 instead.
   const int* kv_table = nullptr;
   int kv_tab_len = 0, kv_page_rows = 0, kv_pages = 0;
+  // Keys and values below the first query were written before the preceding
+  // kernel of the stream started (a model's cache).  False for a caller's
+  // buffers, which that kernel may be writing.
+  bool kv_ready = true;
 };
 
 // Row index (in head-size units) of own slot s of (group g, head h) in a

@@ -1,11 +1,13 @@
 // Kernel launch helper with programmatic dependent launch (PDL).
 //
 // Every kernel of this library calls pdl_wait() before its first global
-// memory access (read or write) and pdl_trigger() once it has started, so a
+// memory access (read or write) and pdl_trigger() once it has started.  The
+// only accesses before the wait are reads of what the host says no preceding
+// kernel can be writing (GemmArgs::w_ready, AttnArgs::kv_ready).  So a
 // kernel launched with the PDL attribute may be scheduled while its
 // predecessor in the stream is still finishing: its launch latency and
 // prologue (barrier init, tensor-memory allocation, descriptor prefetch)
-// overlap the predecessor's tail, while every memory access still happens
+// overlap the predecessor's tail, while every other memory access happens
 // after the predecessor has completed.  Without the attribute both calls
 // are no-ops.
 #pragma once

@@ -92,6 +92,7 @@ int photon_attn_decode_noalloc(int32_t dtype, const void* d_q, const void* d_k, 
   a.O = d_o;
   a.o_ld = (long long)H * head_dim;
   a.scale = 1.0f / sqrtf((float)head_dim);
+  a.kv_ready = false;
   const size_t need = attn_decode_workspace_bytes(dtype, a);
   if (need > kNoAllocScratchBytes) {
     char msg[160];

@@ -2899,6 +2899,7 @@ int photon_gemm(int32_t dtype, const void* d_A, int64_t lda, const void* d_W, in
   g.N = N;
   g.K = K;
   g.ep = epi(EPI_STORE_F32, d_C, ldc);
+  g.w_ready = false;
   if (path == 1) {
     launch_gemm_simt(dtype, g, s);
     CK(cudaGetLastError());
@@ -2950,6 +2951,7 @@ int photon_gemm_rmsnorm(const float* d_x, int64_t ldx, const float* d_g, float e
   g.N = N;
   g.K = K;
   g.ep = epi(EPI_STORE_F32, d_C, ldc);
+  g.w_ready = false;
   if (tma_available() && gemm_tc_fuses_norm(M, N, K)) {
     g.norm_x = d_x;
     g.norm_ld = ldx;
@@ -3028,6 +3030,7 @@ int photon_attn_decode(int32_t dtype, const void* d_q, const void* d_k, const vo
   a.O = d_o;
   a.o_ld = (long long)H * head_dim;
   a.scale = 1.0f / sqrtf((float)head_dim);
+  a.kv_ready = false;
   const size_t wsb = attn_decode_workspace_bytes(dtype, a);
   float* ws = nullptr;
   if (wsb) CK(pool_malloc((void**)&ws, wsb, s));

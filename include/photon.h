@@ -359,7 +359,8 @@ PHOTON_API int photon_export_state(photon_cache* c, int32_t which, int32_t layer
  * path: 0 = the library's choice, 1 = CUDA-core kernel, 2 = tcgen05 kernel
  * (bf16 only; K % 64 == 0, N % 64 == 0).  splits / swap (-1 = automatic)
  * steer the tcgen05 kernel's split-K count and operand swap.  Allocates its
- * split-K scratch internally.  Errors: ERR_ARG (unsupported shape or path). */
+ * split-K scratch internally.  A, W and C may be what the work before it on
+ * the stream writes or reads.  Errors: ERR_ARG (unsupported shape or path). */
 PHOTON_API int photon_gemm(int32_t dtype, const void* d_A, int64_t lda, const void* d_W, int64_t ldw,
                 int32_t M, int32_t N, int32_t K, float* d_C, int64_t ldc, int32_t path,
                 int32_t splits, int32_t swap, void* stream);
@@ -409,6 +410,7 @@ PHOTON_API int photon_attn_prefill(int32_t dtype, const void* d_q, const void* d
  * copies) leaves d_o unwritten and sets *d_err to a nonzero code, which the
  * caller reads after the stream has synchronised (zero it before the call).
  * With d_err NULL such a timeout goes unreported.
+ * The keys and values may be what the work before it on the stream writes.
  * Allocates its split scratch internally.  Errors: ERR_ARG. */
 PHOTON_API int photon_attn_decode(int32_t dtype, const void* d_q, const void* d_k, const void* d_v, int32_t G,
                        int32_t H, int32_t head_dim, int32_t cap, int32_t q_len, int32_t p0,
