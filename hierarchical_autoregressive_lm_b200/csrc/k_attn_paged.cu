@@ -346,8 +346,9 @@ __device__ __forceinline__ void scale_all(float (&o)[N][4], float f) {
 // is divided by the power of two at its largest element; what fp16 cannot
 // hold of it follows times 2^24, so q keeps 22 bits.  A weight p times its
 // scale v has fp32's range, which fp16 has not: p v 2^(15 - x), with a power of
-// two 2^x above every p |v| so far (x = ceil(z - m) for the running maximum z
-// of s + log2 |v|), is at most 2^15, and what fp16 cannot hold of it follows.
+// two 2^x above every p |v| so far (x = ceil(z) for the running maximum z of
+// (s - m) + log2 |v|, in this order: s may be so large that log2 |v| would be
+// lost in its rounding), is at most 2^15, and what fp16 cannot hold of it follows.
 // Weights keep 22 bits down to 2^-17 of the largest, and steps of 2^-38 of the
 // largest below that.
 template <typename T_, typename C, int D, bool PACK>
@@ -447,7 +448,7 @@ struct Half {
 #pragma unroll
       for (int e = 0; e < 2; ++e) to_log2[e] = __shfl_sync(0xffffffffu, f, (2 * t + e) * 4);
     }
-    // columns 2 t, 2 t + 1: maxima of s and of s + log2 |v|, x, sums; rows g, g + 8 of the row tiles
+    // columns 2 t, 2 t + 1: maxima of s and of s - m + log2 |v|, x, sums; rows g, g + 8 of the row tiles
     float m[2] = {-INFINITY, -INFINITY}, z[2] = {-INFINITY, -INFINITY}, x2[2] = {0.f, 0.f}, l[2] = {0.f, 0.f}, o[KS][4];
 #pragma unroll
     for (int n = 0; n < KS; ++n)
@@ -459,12 +460,12 @@ struct Half {
       const uint32_t kt = ring.keys(i), vt = kt + R::kTile;
       const float* const scales = ring.scales(i);
       if constexpr (kNarrow) {
-        // log2 |v| of every position, within +-120, so that no power of two leaves fp32
+        // log2 |v| of every position; below -120 it is raised, so that no power of two leaves fp32
 #pragma unroll
         for (int j = 0; j < R::PL; ++j)
           if (j * 32 + lane < R::TP) {
             const float lv = __log2f(fabsf(scales[R::TP + j * 32 + lane]));
-            const_cast<float*>(scales)[2 * R::TP + j * 32 + lane] = fminf(fmaxf(lv, -120.f), 120.f);
+            const_cast<float*>(scales)[2 * R::TP + j * 32 + lane] = fminf(fmaxf(lv, -120.f), 128.f);
           }
         __syncwarp();
       }
@@ -521,32 +522,38 @@ struct Half {
         }
       }
 
-      float m_new[2], base[2], grow[2], up[2];  // up: 2^(15 - x)
+      float m_new[2], moved[2], grow[2], up[2];  // up: 2^(15 - x)
       bool grown = false;
       largest_of(m_new, s, m);
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const float base = finite_base(m_new[e]);
+        moved[e] = m[e] - base;
+#pragma unroll
+        for (int n = 0; n < 2 * SUB; ++n) s[n][e] -= base;
+      }
       if constexpr (kNarrow) {
-        float sv[2 * SUB][2], z_new[2];
+        float sv[2 * SUB][2];
 #pragma unroll
         for (int n = 0; n < 2 * SUB; ++n) {
           const float lv = scales[2 * R::TP + 8 * n + g];
           sv[n][0] = s[n][0] + lv, sv[n][1] = s[n][1] + lv;
         }
-        largest_of(z_new, sv, z);
-        z[0] = z_new[0], z[1] = z_new[1];
+        const float old[2] = {z[0] + moved[0], z[1] + moved[1]};
+        largest_of(z, sv, old);
       }
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        base[e] = finite_base(m_new[e]);
-        float moved = m[e] - base[e];
+        float by = moved[e];
         if constexpr (kNarrow) {
-          const float x = fminf(fmaxf(ceilf(z[e] - base[e]), -110.f), 121.f);
+          const float x = fminf(fmaxf(ceilf(z[e]), -110.f), 129.f);
           up[e] = __int_as_float((142 - (int)x) << 23);
-          moved += x2[e] - x;
+          by += x2[e] - x;
           grown |= x != x2[e];
           x2[e] = x;
         }
         grown |= m_new[e] != m[e];
-        grow[e] = pow2(moved);
+        grow[e] = pow2(by);
       }
       if (__any_sync(0xffffffffu, grown)) {
 #pragma unroll
@@ -555,14 +562,14 @@ struct Half {
           for (int k = 0; k < 4; ++k) o[n][k] *= grow[k & 1];
       }
 #pragma unroll
-      for (int e = 0; e < 2; ++e) l[e] *= pow2(m[e] - base[e]), m[e] = m_new[e];
+      for (int e = 0; e < 2; ++e) l[e] *= pow2(moved[e]), m[e] = m_new[e];
 
       // the second product's right side: weights of positions 2 t, 2 t + 1 (+ 8) of 16, column g
       auto weights = [&](int u16, uint32_t (&hi)[2], uint32_t (&lo)[2]) {
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
           const int n = 2 * u16 + j;
-          float x = pow2(s[n][0] - base[0]), y = pow2(s[n][1] - base[1]);
+          float x = pow2(s[n][0]), y = pow2(s[n][1]);
           l[0] += x, l[1] += y;
           if constexpr (kNarrow) {
             const float vs = scales[R::TP + 8 * n + g];

@@ -566,6 +566,72 @@ def test_attention_weights_far_apart(kind):
     check_attention(p, table, lens, q)
 
 
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("kind", ["e4m3", "int8"])
+@pytest.mark.parametrize("group", [2, 8])
+def test_attention_largest_values_in_narrow_pages(dtype, kind, group):
+    # rows near the largest number of their type, as the cache write narrows them, and scales beyond those
+    g = gen(73)
+    lens, dim = [1, 30, 1], 64
+    p, table = paged(g, lens, 16, 1, dim, kind)
+    top = torch.finfo(DT[dtype]).max
+    k, v = randn(g, 2, 1, dim).to(DT[dtype]), (randn(g, 2, 1, dim).sign() * top).to(DT[dtype])
+    v[1, 0, ::3] = top / 3
+    k[1] = 30.0
+    hal.kv_write(p, table, ints([0, 7]), k, v, seq=ints([0, 1]))
+    assert (p.v_scale[table[:2, 0].long(), 0, ints([0, 7]).long()] > 2.0 ** (121 if kind == "int8" else 119)).all()
+    code = torch.arange(dim, device="cuda") % 3 - 1.0
+    p.v.view(torch.int8)[table[2, 0].item(), 0, 0] = code.to(DT[kind]).view(torch.int8)
+    p.v_scale[table[2, 0].item(), 0, 0] = 1.9 * 2.0 ** 126
+    q = randn(g, 3, group, dim).to(DT[dtype])
+    q[1] = 1.0  # position 7 takes all the weight: its score is 30 * dim / 8, others' below 60
+    out = torch.empty_like(q)
+    hal.attn_decode_paged(p, table, ints(lens), q, out)
+    want, _, bound, _ = attended(p, table, lens, q, 0, dim ** -0.5)
+    # A result within the bound of `want` may lie beyond the type's largest number, which rounds to infinity: of int8 rows
+    # with fp32's largest number the stored value does so itself, 127 * rn(top / 127) = top (1 + 5.6e-8), and half a step
+    # of top is 3.0e-8 of it.
+    beyond = (want.abs() + bound > top) & out.isinf() & (out.sign() == want.sign())
+    assert off(torch.where(beyond, want, out.double()), want, bound + HALF[dtype] * want.abs() * (1 + 2.0 ** -8)) <= 1
+    assert (beyond.sum(-1) < dim)[1:].all()  # a third of row 1 is a third as large, row 2 ends at 1.9 * 2^126
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("kind", ["e4m3", "int8", "wide"])
+@pytest.mark.parametrize("size", [2.0 ** 20, 2.0 ** 24, 2.0 ** 26, 2.0 ** 40])
+def test_attention_large_scores(dtype, kind, size):
+    # the largest score decides alone, whatever its size and the scale of its value
+    g = gen(79)
+    kind = dtype if kind == "wide" else kind
+    lens, dim = [1, 100, 3000], 64
+    p, table = paged(g, lens, 16, 2, dim, kind)
+    for b, n in enumerate(lens):
+        for h in range(2):
+            at = table[b, (n - 1) // 16].item(), h, (n - 1) % 16
+            if kind in TOP:
+                p.k.view(torch.int8)[at] = torch.ones(dim, device="cuda").to(DT[kind]).view(torch.int8)
+                p.k_scale[at] = size
+            else:
+                p.k[at] = size
+    q = torch.ones(3, 6, dim, device="cuda", dtype=DT[dtype])
+    want = torch.empty(3, 2, dim, dtype=torch.float64, device="cuda")
+    for scale in (1.49, 2.8, 1.99 * 2 ** 20, 2.0 ** -40):
+        for b, n in enumerate(lens):
+            at = table[b, (n - 1) // 16].item(), slice(None), (n - 1) % 16
+            if kind in TOP:
+                p.v_scale[at] = scale
+                want[b] = p.v.view(torch.int8)[at].view(p.v.dtype).double() * float(torch.tensor(scale))
+            else:
+                want[b] = p.v[at].double()
+        out, lse = torch.empty_like(q), torch.empty(3, 6, device="cuda")
+        hal.attn_decode_paged(p, table, ints(lens), q, out, scale=1.0, lse=lse)
+        full = want.repeat_interleave(3, 1)
+        # one weight of 1 in two parts: 2^-17 over bf16 pages, 2^-22 else; the quotient and the rounding
+        bound = (2.0 ** -16 + HALF[dtype]) * full.abs() + 2.0 ** -39 * full.abs().amax(-1, keepdim=True)
+        assert off(out, full, bound) <= 1
+        assert off(lse, torch.full_like(lse, size * dim), 8 * U * size * dim) <= 1
+
+
 def test_bad_lengths_and_pages():
     g = gen(2)
     p, table = paged(g, [32, 32, 32, 32], 8, 1, 64, "bf16")
