@@ -16,8 +16,9 @@
 // Angles.  A pair turns by pos * f turns, f a 64-bit binary fraction.  The
 // product modulo 2^64 drops whole turns without rounding; its upper 32 bits,
 // as a signed number of half-turns in [-1, 1), go to sincospif, whose
-// argument is then off by at most 2^-25 half-turns at any position (fp32
-// pos * f would be off by whole radians near a million).
+// argument is then off by at most 2^-25 half-turns, and by what f was off times
+// the position (2^-28 half-turns at the last one; fp32 pos * f would be off by
+// whole radians near a million).
 #include "kv_pages.cuh"
 #include "launch.cuh"
 

@@ -141,21 +141,24 @@ int photon_rope_frequencies(const photon_rope_config* c, uint64_t* h_freq, float
   if (c->scaling == PHOTON_ROPE_NTK && c->rot_dim < 4) return refuse("rope: NTK scaling needs rot_dim >= 4");
   if (c->scaling == PHOTON_ROPE_YARN && (c->original_len <= 0 || !(c->beta > c->alpha) || !std::isfinite(c->beta - c->alpha)))
     return refuse("rope: YARN needs original_len > 0 and beta > alpha");
-  const double two_pi = 6.283185307179586476925286766559;
-  const double d = c->rot_dim, theta = c->scaling == PHOTON_ROPE_NTK ? c->theta * pow(c->factor, d / (d - 2)) : c->theta;
+  // the fractions have 64 bits, and a position has 31: in doubles f's own
+  // rounding would be as large at the last positions as that of the angle
+  const long double two_pi = 6.283185307179586476925286766559005768L, factor = c->factor, alpha = c->alpha;
+  const long double d = c->rot_dim;
+  const long double theta = c->scaling == PHOTON_ROPE_NTK ? c->theta * powl(factor, d / (d - 2)) : (long double)c->theta;
   for (int i = 0; i < c->rot_dim / 2; ++i) {
-    double f = pow(theta, -2.0 * i / d);
-    if (c->scaling == PHOTON_ROPE_LINEAR) f /= c->factor;
+    long double f = powl(theta, -2 * i / d);
+    if (c->scaling == PHOTON_ROPE_LINEAR) f /= factor;
     if (c->scaling == PHOTON_ROPE_YARN) {
-      double g = (c->original_len * f / two_pi - c->alpha) / (c->beta - c->alpha);
+      long double g = (c->original_len * f / two_pi - alpha) / (c->beta - alpha);
       g = g < 0 ? 0 : g > 1 ? 1 : g;
-      f = f * g + f / c->factor * (1 - g);
+      f = f * g + f / factor * (1 - g);
     }
-    if (!std::isfinite(f)) return refuse("rope: frequency %d is not finite", i);
-    double turns = f / two_pi;
-    turns -= floor(turns);
-    const double scaled_up = rint(turns * 0x1p64);
-    h_freq[i] = scaled_up >= 0x1p64 ? 0 : (uint64_t)scaled_up;
+    if (!std::isfinite((double)f)) return refuse("rope: frequency %d is not finite", i);
+    long double turns = f / two_pi;
+    turns -= floorl(turns);
+    const long double scaled_up = rintl(ldexpl(turns, 64));
+    h_freq[i] = scaled_up >= 0x1p64L ? 0 : (uint64_t)scaled_up;
   }
   *h_scale = (float)(c->attn_scale != 0 ? c->attn_scale : c->scaling == PHOTON_ROPE_YARN ? 0.1 * log(c->factor) + 1 : 1.0);
   return PHOTON_OK;

@@ -668,9 +668,10 @@ typedef struct photon_rope_config {
 
 /* Frequencies of a configuration, on the host (no device is touched):
  * h_freq[i] = f_i / (2 pi) turns a position as a 64-bit binary fraction,
- * round(2^64 * f_i / (2 pi)) modulo 2^64.  The kernels multiply it by the
- * position modulo 2^64, which drops whole turns exactly, so an angle is as
- * accurate at position 2^30 as at 1.  *h_scale receives the scale above.
+ * round(2^64 * f_i / (2 pi)) modulo 2^64, computed in long double (for theta
+ * >= 1 within 2^-60 of a turn).  The kernels multiply it by the position
+ * modulo 2^64, which drops whole turns exactly: an angle is off by 2^-29 turns
+ * more at position 2^31 - 1 than at 1.  *h_scale receives the scale above.
  * Errors: ERR_ARG. */
 PHOTON_API int photon_rope_frequencies(const photon_rope_config* cfg, uint64_t* h_freq, float* h_scale);
 
@@ -687,8 +688,9 @@ typedef struct photon_rope_table {
  * at most 512.  x2 / y2 (heads2 heads, NULL and 0 for none) is a second tensor
  * of the same tokens, for q and k in one launch.  backward != 0 applies the
  * transposed map instead (the gradient of x from that of y).  y may be x (same
- * strides); otherwise the outputs overlap no input.  Angles are exact to
- * fp32 rounding, the arithmetic is fp32, the result is rounded once.
+ * strides); otherwise the outputs overlap no input.  Angles are rounded to
+ * fp32 as half-turns in [-1, 1), by 2^-25 at most; the arithmetic is fp32, the
+ * result is rounded once.
  * tokens = 0 is a no-op.  Errors: ERR_ARG, ERR_CUDA. */
 typedef struct photon_rope_args {
   const photon_rope_table* rope;

@@ -25,6 +25,7 @@ import os
 import subprocess
 import sys
 import threading
+from decimal import Decimal, localcontext
 
 import pytest
 import torch
@@ -127,6 +128,28 @@ def test_rope_strided(dtype, shift):
     hal.rope(r, pos, one, out)
     want, bound = turned(one, pos, r)
     assert off(out, want, bound + HALF[dtype] * want.abs()) <= 1
+
+
+@pytest.mark.parametrize("rot,theta", [(64, 10000.0), (128, 500000.0)])
+def test_rope_at_the_last_positions(rot, theta):
+    """Angles from the formula in 60 digits, not from the library's fractions.
+
+    These may be off by 2^-29 turns, 0.2 u radians, at position 2^31: within the 8 u of a pair, of which the other errors
+    take 6.63.
+    """
+    with localcontext() as ctx:
+        ctx.prec = 60
+        two_pi = 2 * Decimal("3.14159265358979323846264338327950288419716939937510582097494")
+        turns = [Decimal(theta) ** (Decimal(-2 * i) / rot) / two_pi for i in range(rot // 2)]
+        at = [2 ** 31 - 1, 2 ** 31 - 2, 2 ** 30, 2 ** 30 + 12345, 1999999999, -2 ** 31, 1 << 20, 1]
+        ang = torch.tensor([[float(p * f % 1) for f in turns] for p in at], dtype=torch.float64, device="cuda")[:, None, :] * (2 * math.pi)
+    x = randn(gen(83), len(at), 64, rot)
+    out = torch.empty_like(x)
+    hal.rope(hal.Rope(rot, theta=theta), ints(at), x, out)
+    a, b = x.double().chunk(2, -1)
+    want = torch.cat([a * ang.cos() - b * ang.sin(), a * ang.sin() + b * ang.cos()], -1)
+    bound = 8 * U * (a.abs() + b.abs()).repeat(1, 1, 2)
+    assert off(out, want, bound + U * want.abs()) <= 1
 
 
 @pytest.mark.parametrize("inter", [False, True])

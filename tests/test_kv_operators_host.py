@@ -56,6 +56,23 @@ def test_frequencies(kw):
     assert hal.Rope(rot, device="cpu", attn_scale=0.75, **kw).scale == 0.75
 
 
+@pytest.mark.parametrize("kw", [
+    dict(rot=64), dict(rot=2), dict(rot=512), dict(rot=128, theta=500000.0), dict(rot=128, theta=1e7), dict(rot=64, scaling="linear", factor=4.0),
+    dict(rot=128, theta=500000.0, scaling="linear", factor=2.5), dict(rot=64, scaling="ntk", factor=8.0), dict(rot=4, scaling="ntk", factor=1000.0),
+    dict(rot=128, scaling="yarn", factor=32.0, original_len=4096), dict(rot=96, scaling="yarn", factor=2.5, original_len=2048, alpha=2.0, beta=16.0)])
+def test_frequencies_are_right_at_the_last_position(kw):
+    """Within 2^-60 of a turn, 2^-29 turns at position 2^31 - 1, a sixteenth of the angle's rounding to fp32.
+
+    f of at most one radian is 0.16 turns.  Host arithmetic of 64 bits is off by 2^-64 of each result: the power by its
+    exponent's rounding, at most ln(theta factor^2) = 23, and its own 2; the division by 2 pi, the scaling and the blend by
+    fewer than 16 more: 41 * 0.16 + 0.5 units of 2^-64, below 2^-61."""
+    kw = dict(kw)
+    rot = kw.pop("rot")
+    for got, want in zip(hal.Rope(rot, device="cpu", **kw).turns, _turns(rot, **kw)):
+        off = abs(Decimal(got) / 2 ** 64 - want)
+        assert min(off, 1 - off) <= Decimal(2) ** -60
+
+
 def test_rope_config_refusals():
     for kw in (dict(rot_dim=3), dict(rot_dim=0), dict(rot_dim=514), dict(rot_dim=64, theta=0.0), dict(rot_dim=64, theta=float("nan")),
                dict(rot_dim=64, scaling="linear", factor=0.5), dict(rot_dim=2, scaling="ntk", factor=2.0),
