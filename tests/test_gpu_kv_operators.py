@@ -569,6 +569,30 @@ def test_attention_long_sums_have_no_direction(kind, dim):
     assert abs(((out[:4].double() - want) / want).mean().item()) <= 16 * U
 
 
+@pytest.mark.parametrize("kind", ["fp32", "e4m3", "int8"])
+@pytest.mark.parametrize("dim", [32, 64, 128, 256])
+@pytest.mark.parametrize("group", [1, 4, 8])
+def test_attention_fp32_weights_keep_22_bits(kind, dim, group):
+    """Values that are all one: an output is the sum of the weights as the product takes them over the sum that divides it.
+
+    Scores and exponentials cancel.  What is left, in u and for up to four positions: two parts of a weight 2, the tensor
+    cores' four terms cut off 8, sums of the parts and of the weights 1 + 2, the quotient 1: below 16.  Weights of 17 bits
+    would be up to 47 off, of 11 bits 3600.
+    """
+    g = gen(89)
+    lens = [2, 3, 4, 1] * 64
+    p, table = paged(g, lens, 4, 2, dim, kind)
+    for b, n in enumerate(lens):
+        page = table[b, 0].item()
+        p.v.view(torch.int8 if kind in TOP else p.v.dtype)[page, :, :n] = torch.ones((), device="cuda").to(DT[kind]).view(
+            torch.int8 if kind in TOP else p.v.dtype)
+        if kind in TOP:
+            p.v_scale[page, :, :n] = 1
+    q, out = randn(g, len(lens), 2 * group, dim), torch.empty(len(lens), 2 * group, dim, device="cuda")
+    hal.attn_decode_paged(p, table, ints(lens), q, out)
+    assert (out.double() - 1).abs().max().item() <= 16 * U
+
+
 @pytest.mark.parametrize("kind", ["bf16", "e4m3"])
 def test_attention_weights_far_apart(kind):
     # a position that takes nearly all the weight with small values, beside others with large ones
