@@ -354,12 +354,12 @@ bool launch_attn_prefill_path(int dt, const AttnArgs& a, int path, float* part, 
 // n / d for 0 <= n < 2^31 by a multiplication (Granlund and Montgomery 1994,
 // figure 4.1, N = 32): q = (umulhi(n, mul) + n) >> shift.
 struct FastDiv {
-  uint32_t mul, shift, d;
+  uint32_t mul, shift;
 };
 inline FastDiv fast_div(uint32_t d) {
   uint32_t l = 0;
   while ((1ull << l) < d) ++l;
-  return {(uint32_t)(((1ull << 32) * ((1ull << l) - d)) / d + 1), l, d};
+  return {(uint32_t)(((1ull << 32) * ((1ull << l) - d)) / d + 1), l};
 }
 struct RopeArgs {
   const unsigned long long* freq = nullptr;  // turns a position, 64-bit fractions
