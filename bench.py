@@ -1031,7 +1031,9 @@ def measure_prefill_attn_roofline(model, wl, dev, stream) -> dict:
 def measure_attn_roofline(model, wl, dev, stream) -> dict:
     """The top encoder's decode attention alone at the decode's shapes (B
     sequences, H heads, the middle step's key count), all Ltop layers' caches
-    in turn so the 0.86 GB working set exceeds L2."""
+    in turn so the 0.86 GB working set exceeds L2.  Through the kernel-level
+    entry, which reads a caller's keys after the preceding kernel's end only;
+    the model's own steps read cached keys before it."""
     import torch
     import hierarchical_autoregressive_lm_b200 as hal
     s = model.shape

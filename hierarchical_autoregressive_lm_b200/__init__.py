@@ -823,8 +823,9 @@ def _scratch(n: int, device, stream):
 class Rope:
     """Rotary positions (photon_rope_config): the first rot_dim elements of a head turn,
     in pairs (i, i + rot_dim/2), or (2i, 2i + 1) when interleaved.  scaling: "none",
-    "linear", "ntk" or "yarn" with its factor (yarn: original_len, alpha, beta);
-    attn_scale 0 = the scaling's own."""
+    "linear", "ntk" or "yarn" with its factor (yarn: original_len, alpha, beta, blended
+    by the pairs' turns as in arXiv 2309.00071, not by their index); attn_scale 0 = the
+    scaling's own."""
 
     SCALING = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}
 
@@ -1017,7 +1018,8 @@ def attn_decode_paged(pages: KVPages, table, lens, q, out, window: int = 0, scal
     """photon_attn_decode_paged: q, out [sequences, q_heads, head_dim], one new token per
     sequence, over the lens[b] (int32) positions of sequence b (the last `window` of them
     if given).  scale defaults to head_dim ** -0.5; lse: optional fp32 [sequences, q_heads]
-    log-sum-exp of the scaled scores, for joining with attention over other keys."""
+    log-sum-exp of the scaled scores, for joining with attention over other keys.  The work
+    is planned for the table's width: pass table[:, :n] where no length needs more."""
     place = _table(pages, table)
     code, dev = pages._code(q, "q"), pages._dev
     if q.dim() != 3:

@@ -22,11 +22,11 @@
 // Which one a call takes: see choose().
 //
 // Measured on a B200 (copy rate 6.54 TB/s): 64 sequences of 512 to 4096
-// positions, 32 heads over 8 of 128, bf16 pages: 95 us for 605 MB (6.3 TB/s).
-// Two of 131072, e4m3 pages: 92 us for 554 MB (6.0 TB/s; the tile's
+// positions, 32 heads over 8 of 128, bf16 pages: 98 us for 605 MB (6.2 TB/s).
+// Two of 131072, e4m3 pages: 93 us for 554 MB (6.0 TB/s; the tile's
 // instructions and the products' latency take the rest).  fp32 pages, 1024
-// units of 4096 positions of 64: 340 us for 2.15 GB.  One sequence of 257
-// positions, 16 heads of 64: 4.3 us, the latency of length, table, rows and join.
+// units of 4096 positions of 64: 350 us for 2.15 GB.  One sequence of 257
+// positions, 16 heads of 64: 4.7 us, the latency of length, table, rows and join.
 #include <cmath>
 #include <type_traits>
 
@@ -1029,7 +1029,10 @@ constexpr int kJoinSteps = 8;  // what shares cost beyond their steps: the prefi
 // pages, heads of 128, us by clusters and by shares: 8 units of 1024
 // positions 5.5 and 8.7, of 8192 15.4 and 15.1; 32 of 4096 13.0 and 16.4; 512
 // of 512 31 and 33, of 4096 191 and 167).  A step reads about 32 KB whatever
-// the type, so one constant serves them all.
+// the type, so one constant serves them all.  `steps` are those of the table's
+// width or the window, all that the host knows of the lengths: shorter ones
+// behind a wide table take shares where clusters would win (8 units of 1024
+// behind 16384 8.8 us, 128 units 16.4 where clusters take 12.3).
 // Sets plan.cluster, and plan.ctas where shares are better.
 template <class E, int D>
 void choose(Plan& plan, long long units, long long steps) {

@@ -655,7 +655,10 @@ typedef struct photon_rows {
  *   YARN:   (NTK-by-parts, arXiv 2309.00071 section 3.2) f_i * g + f_i /
  *           factor * (1 - g) with g = (r - alpha) / (beta - alpha) clamped to
  *           [0, 1] and r = original_len * f_i / (2 pi), the turns of the
- *           pair within the trained length.
+ *           pair within the trained length.  g is linear in r, as the paper
+ *           defines it.  Checkpoints whose code makes it linear in the pair's
+ *           index i, between two rounded bounds, have other frequencies (up to
+ *           4 times in single pairs): they need a d_freq of their own.
  * scale is attn_scale if that is not 0, else 0.1 ln(factor) + 1 for YARN
  * (section 3.4) and 1 otherwise. */
 enum { PHOTON_ROPE_PLAIN = 0, PHOTON_ROPE_LINEAR = 1, PHOTON_ROPE_NTK = 2, PHOTON_ROPE_YARN = 3 };
@@ -687,8 +690,8 @@ typedef struct photon_rope_table {
  * any sign) for n tokens and `heads` heads of even size head_dim >= rot_dim,
  * at most 512.  x2 / y2 (heads2 heads, NULL and 0 for none) is a second tensor
  * of the same tokens, for q and k in one launch.  backward != 0 applies the
- * transposed map instead (the gradient of x from that of y).  y may be x (same
- * strides); otherwise the outputs overlap no input.  Angles are rounded to
+ * transposed map instead (the gradient of x from that of y).  y may be x (with
+ * the same strides, of one token or head too); otherwise the outputs overlap no input.  Angles are rounded to
  * fp32 as half-turns in [-1, 1), by 2^-25 at most; the arithmetic is fp32, the
  * result is rounded once.
  * tokens = 0 is a no-op.  Errors: ERR_ARG, ERR_CUDA. */
@@ -739,7 +742,7 @@ typedef struct photon_kv_pages {
  * place named twice holds a mixture of the rows).  With `rope`, k is rotated
  * by its position first, in fp32, and q (q_heads heads, NULL and 0 for none)
  * is rotated into q_out in the same launch; q rows of padding
- * tokens are left as they were.  A narrow cache row gets the scale s =
+ * tokens are left as they were, those of tokens without a place are rotated.  A narrow cache row gets the scale s =
  * max(amax, 1e-30) / top with amax its largest magnitude and top = 448 (E4M3)
  * or 127 (INT8), and the codes round(x * (top / max(amax, 1e-30))), to nearest
  * with ties to even; a row that holds an infinity or a NaN reads back as NaN
@@ -777,7 +780,14 @@ PHOTON_API int photon_kv_read(const photon_kv_args* args, void* stream);
  * Softmax statistics and sums are fp32; o must not be q.  Rows behind a
  * length, and pages that no position names, are never read, whatever they
  * hold; an infinity or a NaN within the positions makes the outputs that it
- * reaches infinite or NaN.
+ * reaches infinite or NaN.  What is summed has to stay within fp32: the
+ * largest |scale * q|, q . k, and sum_t exp(s_t - max s) |v_t| before it is
+ * divided.  A score of -infinity weighs nothing; without any weight o = 0 and
+ * lse = -infinity.
+ * The host does not know the lengths: it plans for the table's width (or the
+ * window).  Where a bound on the lengths is known, a width cut down to it (the
+ * stride stays) keeps short contexts on the plan made for them: one sequence
+ * of 257 positions, 8 key heads, 5.4 us, and 10.1 behind a table of 16384.
  * A call that splits long contexts over the whole device needs scratch of a
  * size that its shapes decide (a few MB).  With scratch_bytes 0 the library
  * takes it from its stream-ordered pool and returns it on the stream, as
