@@ -139,7 +139,8 @@ __device__ __forceinline__ void codes_f16(uint32_t& lo, uint32_t& hi, uint32_t w
 // cutting it to 11 bits drops one unit at most, and has either sign.  Rounding
 // by an addition carries a NaN's bits anywhere, but the remainder of what is
 // not finite is NaN, and stays one.  Numbers that would round to infinity are
-// cut off; SMALL: there are none.
+// cut off; SMALL: there are none.  Of numbers below 2^-104 the second part is
+// not a normal one, and may count as zero.
 template <bool SMALL = false>
 __device__ __forceinline__ void split_tf32(uint32_t& hi, uint32_t& lo, float x) {
   uint32_t up = __float_as_uint(x);

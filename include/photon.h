@@ -782,8 +782,9 @@ PHOTON_API int photon_kv_read(const photon_kv_args* args, void* stream);
  * hold; an infinity or a NaN within the positions makes the outputs that it
  * reaches infinite or NaN.  What is summed has to stay within fp32: the
  * largest |scale * q|, q . k, and sum_t exp(s_t - max s) |v_t| before it is
- * divided.  A score of -infinity weighs nothing; without any weight o = 0 and
- * lse = -infinity.
+ * divided; of values below 2^-104, what lies below fp32's normal range may be
+ * lost.  A score of -infinity weighs nothing; without any weight o = 0 and lse
+ * = -infinity.
  * The host does not know the lengths: it plans for the table's width (or the
  * window).  Where a bound on the lengths is known, a width cut down to it (the
  * stride stays) keeps short contexts on the plan made for them: one sequence

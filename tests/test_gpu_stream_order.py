@@ -125,6 +125,54 @@ def test_gemm_rmsnorm_after_a_writer(writer, M):
     check(w, getattr(w, writer), lambda: hal.gemm_rmsnorm(x, gain, w.k[0, H - 1], out), out)
 
 
+@pytest.mark.parametrize("writer", ["write", "read", "rotate"])
+def test_decode_attention_after_a_writer_and_a_product(writer):
+    # a kernel between the two that reads nothing of the first may start, and let the third start, before the first ends
+    g = gen(17)
+    H, cap, dim = 16, 8192, 64
+    w = Writers(g, "bf16", 1, H, cap, dim)
+    q, out = randn(g, "bf16", 1, H * dim), torch.empty(1, H * dim, device="cuda", dtype=torch.bfloat16)
+    A, W, C = randn(g, "bf16", 16, 256), randn(g, "bf16", 128, 256), torch.empty(16, 128, device="cuda")
+
+    def write():
+        getattr(w, writer)()
+        hal.gemm(A, W, C)
+
+    check(w, write, lambda: hal.attn_decode(q, w.k, w.v, 1, cap - 1, out), out)
+
+
+@pytest.mark.parametrize("writer", ["write", "read", "rotate"])
+@pytest.mark.parametrize("entry", ["attn_decode", "gemm"])
+def test_captured_pairs(writer, entry):
+    g = gen(19)
+    H, cap, dim = 16, 8192, 64
+    w = Writers(g, "bf16", 1, H, cap, dim)
+    if entry == "gemm":
+        A, out = randn(g, "bf16", 64, dim), torch.empty(64, cap, device="cuda")
+        reader = lambda: hal.gemm(A, w.k[0, H - 1], out)  # noqa: E731
+    else:
+        q, out = randn(g, "bf16", 1, H * dim), torch.empty(1, H * dim, device="cuda", dtype=torch.bfloat16)
+        reader = lambda: hal.attn_decode(q, w.k, w.v, 1, cap - 1, out)  # noqa: E731
+    w.renew()
+    getattr(w, writer)(), reader()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        getattr(w, writer)()
+        reader()
+    for _ in range(ROUNDS):
+        w.renew()
+        out.fill_(7)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        got = out.clone()
+        reader()
+        torch.cuda.synchronize()
+        assert torch.equal(got, out)
+    del graph
+
+
 def test_decode_attention_after_a_product():
     # fp32 keys and values that are the library's own products
     g = gen(13)
